@@ -197,6 +197,168 @@ seqattn_status seqattn_proj_wgrad(int32_t batch, int64_t seq_len, int64_t row_be
                                   int64_t row_end, int32_t d_model, int32_t n, const void* h,
                                   const float* g, float* dw, seqattn_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The rest of the attention layer: projections, head norm with rotary
+ * positions, and the optimizer step.  (The pages partition the attention and
+ * name the projections only as "chunk i's graph"; these calls run that graph
+ * chunk by chunk around the attention calls.)
+ * ------------------------------------------------------------------------ */
+
+typedef enum {
+  SEQATTN_ACT_NONE = 0,
+  SEQATTN_ACT_RELU = 1,
+  SEQATTN_ACT_SILU = 2,     /* z sigmoid(z) */
+  SEQATTN_ACT_GELU = 3,     /* z Phi(z), by erf */
+  SEQATTN_ACT_GELU_TANH = 4 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+} seqattn_act;
+
+/*
+ * Linear layer, bf16 with float32 sums: a product and its epilogue in one
+ * tensor-core kernel, one rounding to bf16 at the end.
+ *   fwd:    z = x w + bias;  y = act(z) + residual
+ *   dgrad:  dx = act'(z) o (g w^T) + residual
+ *   wgrad:  dw += x^T g;  dbias += sum over rows of g
+ * w: [k, n] dense row-major (the layout of the projections' weight gradients).
+ * x [rows, k], g [rows, n], y, z [rows, n], dx [rows, k] and residual are
+ * row-major with a row stride ld* in elements (so heads of a fused projection
+ * or rows of a cache can be passed as they lie).  dw [k, n] and dbias [n] are
+ * dense float32 and accumulated, in an order fixed by the shapes; calls that
+ * update the same dw or dbias must not overlap.
+ *   fwd:    bias [n], residual and z (out: the pre-activation in bf16, for
+ *           dgrad) may be NULL.
+ *   dgrad:  z is the previous layer's pre-activation, of dx's shape, read
+ *           when act is not NONE (else NULL); residual may be NULL.  g is the
+ *           gradient of this product's own pre-activation.
+ *   wgrad:  dbias may be NULL.
+ * residual may be the output itself (same pointer and stride); no other
+ * overlap of an output with an input is allowed.  Requires k, n and every
+ * stride to be positive multiples of 8, strides at least the row length,
+ * pointers 16-byte aligned, 0 <= rows < 2^31 - 512; rows == 0 is a no-op.
+ * Strides of operands that are NULL are ignored.  No workspace.  Async on
+ * `stream`; INVALID_ARG before any launch on a bad argument.
+ */
+seqattn_status seqattn_linear_fwd(int64_t rows, int32_t k, int32_t n, const void* x, int64_t ldx,
+                                  const void* w, const void* bias, int32_t act,
+                                  const void* residual, int64_t ldr, void* z, int64_t ldz,
+                                  void* y, int64_t ldy, seqattn_stream_t stream);
+seqattn_status seqattn_linear_dgrad(int64_t rows, int32_t k, int32_t n, const void* g, int64_t ldg,
+                                    const void* w, int32_t act, const void* z, int64_t ldz,
+                                    const void* residual, int64_t ldr, void* dx, int64_t lddx,
+                                    seqattn_stream_t stream);
+seqattn_status seqattn_linear_wgrad(int64_t rows, int32_t k, int32_t n, const void* x, int64_t ldx,
+                                    const void* g, int64_t ldg, float* dw, float* dbias,
+                                    seqattn_stream_t stream);
+
+/*
+ * A rotary embedding over the first rot_dim elements of a head.  Pair i is
+ * rotated by position[axis[i]] * turns[i] * 2^-64 turns; turns[i] is the
+ * frequency (f_i / 2 pi, radians per position over 2 pi) as an unsigned 64-bit
+ * fraction, so the angle of any int64 position is exact modulo a turn.  With
+ * interleaved == 0 pair i is elements (i, i + rot_dim / 2), else (2i, 2i + 1).
+ * axes == 1: one position a row; more: several (time, height, width).
+ */
+typedef struct {
+  int32_t rot_dim;      /* multiple of 16, at most head_dim */
+  int32_t axes;         /* 1 .. 64 */
+  int32_t interleaved;  /* 0 or 1 */
+  int32_t reserved;     /* 0 */
+  uint64_t turns[64];   /* rot_dim / 2 used */
+  uint8_t axis[64];     /* each < axes */
+} seqattn_rope_plan;
+
+/*
+ * Between the projections and seqattn_chunk_fwd, for the chunk's rows
+ * [q_start, q_start + q_len): norm every query and key head (RMS over head_dim,
+ * times gamma), rotate it, write the queries to the chunk and the keys and
+ * values into rows [q_start, q_start + q_len) of the caches.
+ *   q_in [B, q_len, Hq, d], k_in, v_in [B, q_len, Hkv, d]: element type pb->dtype,
+ *     heads dense, consecutive rows (b, r) ld_q, ld_k, ld_v elements apart
+ *     (parts of a fused projection's output can be passed in place).
+ *     v_in and v_cache may both be NULL: values are then left alone.
+ *   gamma_q, gamma_k [d]: element type; both NULL: no norm (eps is ignored).
+ *   plan (host): NULL for no rotation.  positions: device int64 [axes, B, q_len],
+ *     or NULL for position q_start + r on every axis.
+ *   q (out) [B, q_len, Hq, d]; k_cache, v_cache (out rows) [B, T, Hkv, d].
+ * The strides are at least a row's length and multiples of 8 elements;
+ * eps >= 0.  Sums, angles and the rotation are in float32, rounded once.
+ */
+seqattn_status seqattn_qk_norm_rope_fwd(const seqattn_problem* pb, int64_t q_start, int64_t q_len,
+                                        const void* q_in, int64_t ld_q, const void* k_in,
+                                        int64_t ld_k, const void* v_in, int64_t ld_v,
+                                        const void* gamma_q, const void* gamma_k, float eps,
+                                        const seqattn_rope_plan* plan, const int64_t* positions,
+                                        void* q, void* k_cache, void* v_cache,
+                                        seqattn_stream_t stream);
+
+/*
+ * Its backward, between seqattn_chunk_bwd (once the chunk's rows of the
+ * accumulators are final) and the projections' gradients: reads dq
+ * [B, q_len, Hq, d] and rows [q_start, q_start + q_len) of dk_accum, dv_accum
+ * [B, T, Hkv, d] (float32) and writes the gradients of q_in, k_in and v_in in
+ * the element type (rows ld_dq, ld_dk, ld_dv elements apart).  dgamma_q,
+ * dgamma_k [d] float32 are accumulated in a fixed order.
+ *   q_in, k_in: the forward's inputs; read for the norm only (NULL without).
+ *   dv_accum and dv_in may both be NULL.
+ *   workspace: device scratch of seqattn_qk_norm_rope_bwd_workspace_size(pb)
+ *     bytes, 256-byte aligned, when there is a norm (else NULL, 0); calls that
+ *     overlap need one each, and must not update the same dgamma.
+ */
+seqattn_status seqattn_qk_norm_rope_bwd(const seqattn_problem* pb, int64_t q_start, int64_t q_len,
+                                        const void* q_in, int64_t ld_q, const void* k_in,
+                                        int64_t ld_k, const void* gamma_q, const void* gamma_k,
+                                        float eps, const seqattn_rope_plan* plan,
+                                        const int64_t* positions, const float* dq,
+                                        const float* dk_accum, const float* dv_accum, void* dq_in,
+                                        int64_t ld_dq, void* dk_in, int64_t ld_dk, void* dv_in,
+                                        int64_t ld_dv, float* dgamma_q, float* dgamma_k,
+                                        void* workspace, size_t workspace_bytes,
+                                        seqattn_stream_t stream);
+
+/* Bytes of workspace seqattn_qk_norm_rope_bwd needs (0 for an invalid problem). */
+size_t seqattn_qk_norm_rope_bwd_workspace_size(const seqattn_problem* pb);
+
+/* One tensor of an optimizer step.  Pointers are device pointers, 16-byte
+ * aligned (the scales: 4-byte aligned). */
+typedef struct {
+  float* param;          /* [n] float32 master weights, updated */
+  void* lowp;            /* [n] bf16 copy of the updated param, or NULL */
+  const void* grad;      /* [n] float32 or bf16 */
+  void* m;               /* first moment: [n] float32, or e4m3 codes (8 bit) */
+  void* v;               /* second moment: [n] float32, or e4m3 codes of its root */
+  float* m_scale;        /* 8 bit: [ceil(n / 256)] scale of each 256 elements */
+  float* v_scale;
+  int64_t n;             /* >= 0 */
+  float weight_decay;    /* finite */
+  int32_t grad_bf16;     /* 0: grad is float32, 1: bf16 */
+} seqattn_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, grad_scale;
+  int64_t step;                 /* 1 for the first step */
+  const float* lr_dev;          /* device scalars read when the step runs: lr_dev and */
+  const float* grad_scale_dev;  /* step_dev replace lr and step, grad_scale_dev is */
+  const int64_t* step_dev;      /* multiplied to grad_scale.  NULL: the host values. */
+} seqattn_adamw_params;
+
+/*
+ * One AdamW step (decoupled weight decay) over `count` tensors:
+ *   g = grad_scale grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - lr weight_decay)
+ *           - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * state_bits 32: m and v float32.  state_bits 8: m and u = sqrt(v) are kept as
+ * e4m3 codes of m / m_scale and u / v_scale, m_scale and v_scale being the
+ * largest magnitude of each 256 consecutive elements over 448; a positive u is
+ * never stored as zero, and a block whose largest magnitude is under 1e-30
+ * stores zeros.  Zeroed states (codes and scales) are the initial ones.
+ * The descriptors (host memory) are read during the call and travel with the
+ * launch; a captured call keeps the values it was captured with, so a step
+ * meant for replay passes step_dev (and lr_dev).  No two tensors of a call may
+ * overlap.  0 <= beta1, beta2 < 1, eps >= 0; lr, eps and grad_scale finite, step >= 1.
+ */
+seqattn_status seqattn_adamw_step(const seqattn_adamw_tensor* tensors, int32_t count,
+                                  int32_t state_bits, const seqattn_adamw_params* params,
+                                  seqattn_stream_t stream);
+
 /* Bytes of workspace seqattn_chunk_bwd needs for a chunk of q_len rows
  * (0 for an invalid problem).  Pure host function. */
 size_t seqattn_bwd_workspace_size(const seqattn_problem* pb, int64_t q_len);

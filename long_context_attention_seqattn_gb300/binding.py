@@ -10,7 +10,9 @@ not been built, the first call raises; there is no other code path.
 """
 
 import ctypes
+import math
 import os
+from fractions import Fraction
 
 import torch
 
@@ -32,6 +34,13 @@ EXPORTED = (
     "seqattn_reset_accum",
     "seqattn_scale_accum_rows",
     "seqattn_proj_wgrad",
+    "seqattn_linear_fwd",
+    "seqattn_linear_dgrad",
+    "seqattn_linear_wgrad",
+    "seqattn_qk_norm_rope_fwd",
+    "seqattn_qk_norm_rope_bwd",
+    "seqattn_qk_norm_rope_bwd_workspace_size",
+    "seqattn_adamw_step",
     "seqattn_bwd_workspace_size",
     "seqattn_sync_status",
     "seqattn_set_wait_limit",
@@ -49,6 +58,49 @@ class Problem(ctypes.Structure):
         ("head_dim", ctypes.c_int32),
         ("seq_capacity", ctypes.c_int64),
         ("dtype", ctypes.c_int32),
+    ]
+
+
+class RopePlan(ctypes.Structure):
+    """Mirror of ``seqattn_rope_plan`` (made by ``rope_plan``)."""
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32),
+        ("axes", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("turns", ctypes.c_uint64 * 64),
+        ("axis", ctypes.c_uint8 * 64),
+    ]
+
+
+class AdamwTensor(ctypes.Structure):
+    """Mirror of ``seqattn_adamw_tensor``."""
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("lowp", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("weight_decay", ctypes.c_float),
+        ("grad_bf16", ctypes.c_int32),
+    ]
+
+
+class AdamwParams(ctypes.Structure):
+    """Mirror of ``seqattn_adamw_params``."""
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("grad_scale", ctypes.c_double),
+        ("step", ctypes.c_int64),
+        ("lr_dev", ctypes.c_void_p),
+        ("grad_scale_dev", ctypes.c_void_p),
+        ("step_dev", ctypes.c_void_p),
     ]
 
 
@@ -86,6 +138,23 @@ def load_library(path=LIB_PATH):
     i32 = ctypes.c_int32
     lib.seqattn_proj_wgrad.argtypes = [i32, i64, i64, i64, i32, i32, vp, vp, vp, vp]
     lib.seqattn_proj_wgrad.restype = ctypes.c_int
+    lib.seqattn_linear_fwd.argtypes = [i64, i32, i32, vp, i64, vp, vp, i32, vp, i64, vp, i64, vp, i64, vp]
+    lib.seqattn_linear_fwd.restype = ctypes.c_int
+    lib.seqattn_linear_dgrad.argtypes = [i64, i32, i32, vp, i64, vp, i32, vp, i64, vp, i64, vp, i64, vp]
+    lib.seqattn_linear_dgrad.restype = ctypes.c_int
+    lib.seqattn_linear_wgrad.argtypes = [i64, i32, i32, vp, i64, vp, i64, vp, vp, vp]
+    lib.seqattn_linear_wgrad.restype = ctypes.c_int
+    R = ctypes.POINTER(RopePlan)
+    lib.seqattn_qk_norm_rope_fwd.argtypes = [P, i64, i64, vp, i64, vp, i64, vp, i64, vp, vp, f32, R, vp, vp, vp,
+                                             vp, vp]
+    lib.seqattn_qk_norm_rope_fwd.restype = ctypes.c_int
+    lib.seqattn_qk_norm_rope_bwd.argtypes = [P, i64, i64, vp, i64, vp, i64, vp, vp, f32, R, vp, vp, vp, vp, vp,
+                                             i64, vp, i64, vp, i64, vp, vp, vp, sz, vp]
+    lib.seqattn_qk_norm_rope_bwd.restype = ctypes.c_int
+    lib.seqattn_qk_norm_rope_bwd_workspace_size.argtypes = [P]
+    lib.seqattn_qk_norm_rope_bwd_workspace_size.restype = sz
+    lib.seqattn_adamw_step.argtypes = [ctypes.POINTER(AdamwTensor), i32, i32, ctypes.POINTER(AdamwParams), vp]
+    lib.seqattn_adamw_step.restype = ctypes.c_int
     lib.seqattn_bwd_workspace_size.argtypes = [P, i64]
     lib.seqattn_bwd_workspace_size.restype = sz
     lib.seqattn_sync_status.argtypes = [vp]
@@ -224,6 +293,367 @@ def proj_wgrad(h, g, dw, row_begin, row_end, stream=None):
         raise ValueError(f"g has leading shape {tuple(g.shape[:2])}, expected {(B, T)}")
     _check(load_library().seqattn_proj_wgrad(B, T, row_begin, row_end, dm, n, _ptr(h), _ptr(g), _ptr(dw),
                                              _stream(stream)))
+
+
+# ------------------------------------------------------------------ the rest of the layer
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _act_code(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}, expected one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def _here(t, name, dtype):
+    """``t`` is a CUDA tensor of ``dtype`` on the current device."""
+    if not t.is_cuda or t.dtype != dtype:
+        raise ValueError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _matrix(t, name, cols=None, rows=None, dtype=torch.bfloat16):
+    """(rows, columns, row stride) of a tensor seen as a matrix of its last
+    dimension; the leading dimensions must lie at one uniform row stride."""
+    _here(t, name, dtype)
+    shape, stride = t.shape, t.stride()
+    if len(shape) < 2:
+        raise ValueError(f"{name} must have at least two dimensions")
+    c = shape[-1]
+    if c > 1 and stride[-1] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    r, ld = 1, None
+    for size, st in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if size == 0:
+            r = 0
+            break
+        if size == 1:
+            continue
+        if ld is None:
+            ld = st
+        elif st != r * ld:
+            raise ValueError(f"the rows of {name} must lie at one uniform stride")
+        r *= size
+    if cols is not None and c != cols:
+        raise ValueError(f"{name} has {c} columns, expected {cols}")
+    if rows is not None and r != rows:
+        raise ValueError(f"{name} has {r} rows, expected {rows}")
+    return r, c, c if ld is None else ld
+
+
+def _weight(w):
+    _here(w, "w", torch.bfloat16)
+    if w.dim() != 2 or not w.is_contiguous():
+        raise ValueError("w must be a contiguous [k, n] matrix")
+    return w.shape
+
+
+def _vector(t, name, n, dtype):
+    _here(t, name, dtype)
+    if tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} elements")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+
+
+def linear_fwd(x, w, y, bias=None, act="none", residual=None, z=None, stream=None):
+    """y = act(x w + bias) + residual, rounded to bf16 once.  ``x`` [..., k],
+    ``y``, ``residual`` [..., n] bf16 with rows at a uniform stride, ``w``
+    [k, n] and ``bias`` [n] bf16.  ``z`` [..., n] bf16, if given, receives the
+    pre-activation x w + bias.  ``residual`` may be ``y``."""
+    k, n = _weight(w)
+    rows, _, ldx = _matrix(x, "x", k)
+    _, _, ldy = _matrix(y, "y", n, rows)
+    ldr = ldz = 0
+    if bias is not None:
+        _vector(bias, "bias", n, torch.bfloat16)
+    if residual is not None:
+        _, _, ldr = _matrix(residual, "residual", n, rows)
+    if z is not None:
+        _, _, ldz = _matrix(z, "z", n, rows)
+    _check(load_library().seqattn_linear_fwd(rows, k, n, x.data_ptr(), ldx, w.data_ptr(), _addr(bias),
+                                             _act_code(act), _addr(residual), ldr, _addr(z), ldz, y.data_ptr(), ldy,
+                                             _raw_stream(stream)))
+
+
+def linear_dgrad(g, w, dx, act="none", z=None, residual=None, stream=None):
+    """dx = act'(z) o (g w^T) + residual, rounded to bf16 once: the gradient of
+    a linear layer's input, times the derivative of the activation that made
+    the input when ``act`` is given (``z``: that activation's argument, as
+    ``linear_fwd`` of the layer before kept it).  ``g`` [..., n], ``dx``,
+    ``z``, ``residual`` [..., k] bf16, ``w`` [k, n].  ``residual`` may be
+    ``dx`` (several gradients of one input are summed that way)."""
+    k, n = _weight(w)
+    code = _act_code(act)
+    rows, _, ldg = _matrix(g, "g", n)
+    _, _, lddx = _matrix(dx, "dx", k, rows)
+    ldr = ldz = 0
+    if residual is not None:
+        _, _, ldr = _matrix(residual, "residual", k, rows)
+    if code:
+        if z is None:
+            raise ValueError("z is needed when act is given")
+        _, _, ldz = _matrix(z, "z", k, rows)
+    _check(load_library().seqattn_linear_dgrad(rows, k, n, g.data_ptr(), ldg, w.data_ptr(), code,
+                                               z.data_ptr() if code else None, ldz, _addr(residual), ldr,
+                                               dx.data_ptr(), lddx, _raw_stream(stream)))
+
+
+def linear_wgrad(x, g, dw, dbias=None, stream=None):
+    """dw += x^T g and dbias += the column sums of g.  ``x`` [..., k], ``g``
+    [..., n] bf16 with rows at a uniform stride, ``dw`` [k, n] and ``dbias``
+    [n] float32, accumulated.  (``proj_wgrad`` is the form for float32 g of
+    whole [B, T, ...] gradients.)"""
+    rows, k, ldx = _matrix(x, "x")
+    _, n, ldg = _matrix(g, "g", None, rows)
+    _here(dw, "dw", torch.float32)
+    if tuple(dw.shape) != (k, n) or not dw.is_contiguous():
+        raise ValueError(f"dw must be a contiguous [{k}, {n}] matrix")
+    if dbias is not None:
+        _vector(dbias, "dbias", n, torch.float32)
+    _check(load_library().seqattn_linear_wgrad(rows, k, n, x.data_ptr(), ldx, g.data_ptr(), ldg, dw.data_ptr(),
+                                               _addr(dbias), _raw_stream(stream)))
+
+
+def rope_plan(inv_freq, axis=None, interleaved=False):
+    """Rotary plan of ``2 len(inv_freq)`` elements: pair i turns by
+    ``inv_freq[i]`` radians a position of axis ``axis[i]`` (default: one axis).
+    ``interleaved``: pair i is elements (2i, 2i + 1) instead of
+    (i, i + len(inv_freq)).  The frequencies are kept as 64-bit fractions of a
+    turn, so the angle of any position is exact modulo a turn."""
+    pairs = len(inv_freq)
+    if pairs < 8 or pairs > 64 or pairs % 8:
+        raise ValueError("inv_freq must have a multiple of 8 entries, at most 64")
+    axis = [0] * pairs if axis is None else [int(a) for a in axis]
+    if len(axis) != pairs or min(axis) < 0 or max(axis) > 63:
+        raise ValueError("axis must give each pair an axis in [0, 64)")
+    plan = RopePlan(rot_dim=2 * pairs, axes=max(axis) + 1, interleaved=int(bool(interleaved)), reserved=0)
+    for i, f in enumerate(inv_freq):
+        f = float(f)
+        if not math.isfinite(f):
+            raise ValueError(f"inv_freq[{i}] is not finite")
+        # f / 2 pi in units of 2^-64, modulo a turn (2 pi to 40 digits: no double rounding)
+        plan.turns[i] = round(Fraction(f) / _TWO_PI * 2 ** 64) % 2 ** 64
+        plan.axis[i] = axis[i]
+    return plan
+
+
+_TWO_PI = Fraction(6283185307179586476925286766559005768394, 10 ** 39)
+
+
+def _head_rows(t, name, B, c, H, d, dtype):
+    """Row stride of a [B, c, H, d] tensor whose heads are dense and whose rows
+    (b, r) lie at one uniform stride."""
+    _here(t, name, dtype)
+    if tuple(t.shape) != (B, c, H, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, c, H, d)}")
+    sb, sc, sh, sd = t.stride()
+    if sd != 1 or (H > 1 and sh != d):
+        raise ValueError(f"the heads of {name} must be dense")
+    if c == 0:
+        return H * d
+    if c > 1:
+        if B > 1 and sb != c * sc:
+            raise ValueError(f"the rows of {name} must lie at one uniform stride")
+        return sc
+    return sb if B > 1 else H * d
+
+
+def _rope_args(q, k_like, gamma_q, gamma_k, plan, positions, dtype):
+    """Problem, shape and pointers that the forward and backward share."""
+    B, c, Hq, d = q.shape
+    Bk, T, Hkv, dk = k_like.shape
+    if Bk != B or dk != d:
+        raise ValueError(f"caches of shape {tuple(k_like.shape)} do not go with queries of shape {tuple(q.shape)}")
+    if (gamma_q is None) != (gamma_k is None):
+        raise ValueError("gamma_q and gamma_k must both be given or both be None")
+    if gamma_q is not None:
+        _vector(gamma_q, "gamma_q", d, dtype)
+        _vector(gamma_k, "gamma_k", d, dtype)
+    if positions is not None:
+        axes = plan.axes if plan is not None else 1
+        _here(positions, "positions", torch.int64)
+        if positions.dim() == 2 and axes == 1:
+            positions = positions[None]
+        if tuple(positions.shape) != (axes, B, c) or not positions.is_contiguous():
+            raise ValueError(f"positions must be a contiguous int64 tensor of shape {(axes, B, c)}")
+    return Problem(B, Hq, Hkv, d, T, _dtype_code(dtype)), B, c, Hq, Hkv, d, positions
+
+
+def qk_norm_rope_fwd(q_in, k_in, v_in, q, k_cache, v_cache, q_start, gamma_q=None, gamma_k=None, eps=1e-6,
+                     plan=None, positions=None, stream=None):
+    """From the projections to the attention, for the chunk whose rows are
+    [q_start, q_start + c): RMS norm of every query and key head (times
+    ``gamma_q``, ``gamma_k`` [d]; without them no norm), rotary positions
+    (``plan`` of ``rope_plan``; without it no rotation), queries to ``q``
+    [B, c, Hq, d], keys and values into those rows of ``k_cache``, ``v_cache``
+    [B, T, Hkv, d].  ``q_in`` [B, c, Hq, d], ``k_in``, ``v_in`` [B, c, Hkv, d]
+    may be parts of a fused projection's output (dense heads, uniform row
+    stride); ``v_in`` and ``v_cache`` may both be None.  ``positions``: int64
+    [axes, B, c] (or [B, c]); by default row r is at position q_start + r."""
+    dt = q.dtype
+    pb, B, c, Hq, Hkv, d, positions = _rope_args(q, k_cache, gamma_q, gamma_k, plan, positions, dt)
+    ldq = _head_rows(q_in, "q_in", B, c, Hq, d, dt)
+    ldk = _head_rows(k_in, "k_in", B, c, Hkv, d, dt)
+    if (v_in is None) != (v_cache is None):
+        raise ValueError("v_in and v_cache must both be given or both be None")
+    ldv = 0
+    _here(q, "q", dt)
+    _need(q, "q", dt)
+    _here(k_cache, "k_cache", dt)
+    _need(k_cache, "k_cache", dt)
+    if v_in is not None:
+        ldv = _head_rows(v_in, "v_in", B, c, Hkv, d, dt)
+        _here(v_cache, "v_cache", dt)
+        _need(v_cache, "v_cache", dt, k_cache.shape)
+    _check(load_library().seqattn_qk_norm_rope_fwd(
+        pb, q_start, c, q_in.data_ptr(), ldq, k_in.data_ptr(), ldk, _addr(v_in), ldv, _addr(gamma_q),
+        _addr(gamma_k), eps, plan, _addr(positions), q.data_ptr(), k_cache.data_ptr(), _addr(v_cache),
+        _raw_stream(stream)))
+
+
+def qk_norm_rope_bwd_workspace_size(head_dim):
+    return int(load_library().seqattn_qk_norm_rope_bwd_workspace_size(Problem(1, 1, 1, head_dim, 1, SEQATTN_BF16)))
+
+
+def qk_norm_rope_bwd(q_in, k_in, dq, dk_accum, dv_accum, dq_in, dk_in, dv_in, q_start, gamma_q=None, gamma_k=None,
+                     dgamma_q=None, dgamma_k=None, eps=1e-6, plan=None, positions=None, workspace=None,
+                     stream=None):
+    """Backward of ``qk_norm_rope_fwd``: from ``dq`` [B, c, Hq, d] and rows
+    [q_start, q_start + c) of ``dk_accum``, ``dv_accum`` [B, T, Hkv, d]
+    (float32, final) to ``dq_in``, ``dk_in``, ``dv_in`` in the element type
+    (they may be parts of one fused gradient).  With a norm, ``q_in`` and
+    ``k_in`` are the forward's inputs and ``dgamma_q``, ``dgamma_k`` [d]
+    float32 are accumulated; ``workspace`` is a uint8 CUDA tensor of at least
+    ``qk_norm_rope_bwd_workspace_size(d)`` bytes (allocated here when
+    omitted).  ``dv_accum`` and ``dv_in`` may both be None."""
+    dt = dq_in.dtype
+    pb, B, c, Hq, Hkv, d, positions = _rope_args(dq, dk_accum, gamma_q, gamma_k, plan, positions, dt)
+    _here(dq, "dq", torch.float32)
+    _need(dq, "dq", torch.float32)
+    _here(dk_accum, "dk_accum", torch.float32)
+    _need(dk_accum, "dk_accum", torch.float32)
+    lddq = _head_rows(dq_in, "dq_in", B, c, Hq, d, dt)
+    lddk = _head_rows(dk_in, "dk_in", B, c, Hkv, d, dt)
+    if (dv_accum is None) != (dv_in is None):
+        raise ValueError("dv_accum and dv_in must both be given or both be None")
+    lddv = ldq = ldk = ws_bytes = 0
+    if dv_in is not None:
+        lddv = _head_rows(dv_in, "dv_in", B, c, Hkv, d, dt)
+        _here(dv_accum, "dv_accum", torch.float32)
+        _need(dv_accum, "dv_accum", torch.float32, dk_accum.shape)
+    norm = gamma_q is not None
+    temp = False
+    if norm:
+        ldq = _head_rows(q_in, "q_in", B, c, Hq, d, dt)
+        ldk = _head_rows(k_in, "k_in", B, c, Hkv, d, dt)
+        if dgamma_q is None or dgamma_k is None:
+            raise ValueError("dgamma_q and dgamma_k are needed with a norm")
+        _vector(dgamma_q, "dgamma_q", d, torch.float32)
+        _vector(dgamma_k, "dgamma_k", d, torch.float32)
+        temp = workspace is None
+        if temp:
+            workspace = torch.empty(qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=dq.device)
+        else:
+            _here(workspace, "workspace", torch.uint8)
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous")
+        ws_bytes = workspace.numel()
+    _check(load_library().seqattn_qk_norm_rope_bwd(
+        pb, q_start, c, _addr(q_in) if norm else None, ldq, _addr(k_in) if norm else None, ldk, _addr(gamma_q),
+        _addr(gamma_k), eps, plan, _addr(positions), dq.data_ptr(), dk_accum.data_ptr(), _addr(dv_accum),
+        dq_in.data_ptr(), lddq, dk_in.data_ptr(), lddk, _addr(dv_in), lddv, _addr(dgamma_q) if norm else None,
+        _addr(dgamma_k) if norm else None, _addr(workspace) if norm else None, ws_bytes, _raw_stream(stream)))
+    if temp and stream is not None:
+        workspace.record_stream(stream)       # as in chunk_bwd
+
+
+class AdamW:
+    """AdamW over many tensors, one launch a step (a few for hundreds of
+    tensors).  ``params``: float32 master weights; ``grads``: their gradients
+    (float32 or bf16), read at every step from the same tensors; ``lowp``: bf16
+    copies that every step rewrites (or None, or None entries).  ``state_bits``
+    32 keeps both moments in float32, 8 keeps e4m3 codes with a float32 scale
+    for each 256 elements: m, and the square root of v.  The states are
+    allocated zeroed, or taken from ``m``, ``v`` (and ``m_scale``,
+    ``v_scale``), lists as long as ``params``.  ``weight_decay``: one number
+    or one per tensor.  All tensors contiguous, on one device."""
+
+    def __init__(self, params, grads, lowp=None, state_bits=32, weight_decay=0.0, m=None, v=None, m_scale=None,
+                 v_scale=None):
+        count = len(params)
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits {state_bits} is not 8 or 32")
+        given = (m, v, m_scale, v_scale) if state_bits == 8 else (m, v)
+        if any(s is None for s in given) and any(s is not None for s in given):
+            raise ValueError("the states must all be given or all be left out")
+        if state_bits == 32 and (m_scale is not None or v_scale is not None):
+            raise ValueError("32-bit states have no scales")
+        lowp = [None] * count if lowp is None else list(lowp)
+        decay = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * count
+        for name, lst in (("grads", grads), ("lowp", lowp), ("weight_decay", decay), ("m", m), ("v", v),
+                          ("m_scale", m_scale), ("v_scale", v_scale)):
+            if lst is not None and len(lst) != count:
+                raise ValueError(f"{name} has {len(lst)} entries, expected {count}")
+        state = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        if m is None:
+            m = [torch.zeros(p.shape, dtype=torch.float32, device=p.device).to(state) for p in params]
+            v = [torch.zeros(p.shape, dtype=torch.float32, device=p.device).to(state) for p in params]
+            if state_bits == 8:
+                m_scale = [torch.zeros(-(-p.numel() // 256), device=p.device) for p in params]
+                v_scale = [torch.zeros(-(-p.numel() // 256), device=p.device) for p in params]
+        none = [None] * count
+        self.state_bits = state_bits
+        self.params, self.grads, self.lowp, self.m, self.v = list(params), list(grads), lowp, list(m), list(v)
+        self.m_scale = none if m_scale is None else list(m_scale)
+        self.v_scale = none if v_scale is None else list(v_scale)
+        self.device = params[0].device if count else None
+        self._tensors = (AdamwTensor * count)()
+        for i, (p, g, lo, mi, vi, ms, vs, wd) in enumerate(zip(self.params, self.grads, self.lowp, self.m, self.v,
+                                                              self.m_scale, self.v_scale, decay)):
+            n = p.numel()
+            if g.dtype not in (torch.float32, torch.bfloat16):
+                raise TypeError(f"grads[{i}] must be float32 or bfloat16")
+            for name, t, dtype, size in (("params", p, torch.float32, n), ("grads", g, g.dtype, n),
+                                         ("lowp", lo, torch.bfloat16, n), ("m", mi, state, n), ("v", vi, state, n),
+                                         ("m_scale", ms, torch.float32, -(-n // 256)),
+                                         ("v_scale", vs, torch.float32, -(-n // 256))):
+                if t is None:
+                    continue
+                _need(t, f"{name}[{i}]", dtype)
+                if t.numel() != size or t.device != self.device:
+                    raise ValueError(f"{name}[{i}] must have {size} elements on {self.device}")
+            self._tensors[i] = AdamwTensor(_addr(p), _addr(lo), _addr(g), _addr(mi), _addr(vi), _addr(ms), _addr(vs),
+                                           n, float(wd), int(g.dtype == torch.bfloat16))
+
+    def step(self, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, grad_scale=1.0, stream=None):
+        """One step; ``step`` counts from 1.  ``lr``, ``step`` and
+        ``grad_scale`` may be one-element CUDA tensors (float32, int64,
+        float32), read when the step runs: what a captured graph needs, since
+        numbers are kept as they were at the capture."""
+        if self.device is not None and self.device.index != torch.cuda.current_device():
+            raise ValueError(f"the tensors are on {self.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        a = AdamwParams(0.0, beta1, beta2, eps, 1.0, 0, None, None, None)
+        for name, value, dtype in (("lr", lr, torch.float32), ("grad_scale", grad_scale, torch.float32),
+                                   ("step", step, torch.int64)):
+            if isinstance(value, torch.Tensor):
+                _here(value, name, dtype)
+                if value.numel() != 1:
+                    raise ValueError(f"{name} must have one element")
+                setattr(a, name + "_dev", value.data_ptr())
+            else:
+                setattr(a, name, value)
+        _check(load_library().seqattn_adamw_step(self._tensors, len(self.params), self.state_bits, a,
+                                                 _raw_stream(stream)))
 
 
 def sync_status(stream=None):

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -69,5 +70,78 @@ struct WgradMaps {
 cudaError_t launch_wgrad_bf16(const WgradMaps& maps, int32_t batch, int64_t row_begin, int64_t row_end,
                               int32_t d_model, int32_t n, unsigned int* err, long long wait_cycles,
                               cudaStream_t s);
+
+// ---- linear layer: products with epilogues (tcgen05) ------------------------
+enum : int { kLinearFwd = 0, kLinearDgrad = 1, kLinearWgrad = 2 };
+enum : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+// Contraction elements per pipeline stage; operand boxes are {64, 128 rows}
+// for an operand whose contraction index is contiguous, else {64, 64 rows},
+// 128-byte swizzle.
+constexpr int kLinearStageK = 64;
+struct LinearMaps {
+  CUtensorMap a, b;
+};
+struct LinearParams {
+  int m, n, k;                 // result rows and columns, contraction length
+  int act;
+  const __nv_bfloat16* bias;   // [n], forward
+  const __nv_bfloat16* residual;
+  __nv_bfloat16* z;            // pre-activation: written by the forward, read by dgrad
+  void* out;                   // bf16 (forward, dgrad) or float32 accumulator (wgrad)
+  int64_t ldr, ldz, ldo;       // row strides in elements
+  unsigned int* err;
+  long long wait_cycles;
+};
+cudaError_t launch_linear_bf16(int mode, const LinearMaps& maps, const LinearParams& p, cudaStream_t s);
+// dbias[j] += sum over rows of g[r, j] (bf16), in a fixed order
+cudaError_t launch_colsum_bf16(const void* g, int64_t ldg, int rows, int n, float* dbias, cudaStream_t s);
+
+// ---- head norm + rotary positions + cache write ------------------------------
+struct NormRopeParams {
+  int B, q_len, Hq, Hkv;
+  int64_t T, q_start;
+  // forward: x = q/k/v inputs, y = q chunk and caches; backward: see the kernel
+  const void *q_in, *k_in, *v_in;      // element type, rows of `*_stride` elements
+  int64_t q_stride, k_stride, v_stride;
+  const void *gamma_q, *gamma_k;       // element type [d], or NULL
+  float eps;
+  const int64_t* positions;            // [axes, B, q_len], or NULL (q_start + row)
+  void *q, *k_cache, *v_cache;         // forward outputs
+  const float *dq, *dk, *dv;           // backward inputs
+  void *dq_in, *dk_in, *dv_in;         // backward outputs, rows of `d*_stride` elements
+  int64_t dq_stride, dk_stride, dv_stride;
+  float* partial;                      // backward: [blocks, 2, d] partial dgamma
+  float *dgamma_q, *dgamma_k;
+  int rot_dim, axes, interleaved;      // rot_dim 0: no rotation
+  uint64_t turns[64];                  // turns per position, in units of 2^-64
+  uint8_t axis[64];
+};
+cudaError_t launch_norm_rope_fwd(const NormRopeParams& p, int d, bool bf16, cudaStream_t s);
+// most blocks of the backward's grid, and so rows of `partial`
+int norm_rope_bwd_blocks();
+cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, int d, bool bf16, cudaStream_t s);
+
+// ---- AdamW over many tensors ---------------------------------------------------
+struct AdamwTensor {          // mirrors seqattn_adamw_tensor
+  float* param;
+  void* lowp;                 // bf16 copy of param, or NULL
+  const void* grad;
+  void *m, *v;                // float32, or e4m3 codes
+  float *m_scale, *v_scale;   // 8-bit states: one scale per 256 elements
+  int64_t n;
+  float weight_decay;
+  int32_t grad_bf16;
+};
+struct AdamwHyper {
+  float lr, beta1, one_minus_beta1, beta2, one_minus_beta2, eps, grad_scale;
+  float step_size, inv_root_bc2;   // lr / (1 - beta1^step), 1 / sqrt(1 - beta2^step)
+  double lrd, beta1d, beta2d;
+  int64_t step;
+  const float* lr_dev;             // device values that replace the host's, or NULL
+  const float* grad_scale_dev;
+  const int64_t* step_dev;
+};
+constexpr int kAdamwBlock = 256;   // elements per 8-bit scale
+cudaError_t launch_adamw(const AdamwTensor* t, int count, int state_bits, const AdamwHyper& h, cudaStream_t s);
 
 }  // namespace seqattn

@@ -1,7 +1,8 @@
 // seqattn_api.cu -- the C ABI declared in include/seqattn.h: argument
 // validation (before any launch), TMA tensor maps, the per-device error word,
 // and dispatch to the float32 and bf16 kernel families, the accumulator row
-// scaling and the projection weight gradient kernel.
+// scaling, the projection weight gradient kernel, the linear layer's products,
+// the head norm with rotary positions and the optimizer step.
 #include <cudaTypedefs.h>
 #include <math.h>
 #include <stdarg.h>
@@ -470,3 +471,360 @@ extern "C" seqattn_status seqattn_chunk_bwd_noalloc(
   e = launch_bwd_bf16(g, maps, delta, dq, dk_accum, dv_accum, err, st);
   return e == cudaSuccess ? ok() : cuda_fail(e, "bwd_bf16 launch");
 }
+
+// ---------------------------------------------------------------------------
+// The rest of the layer: linear products, head norm + rotary positions, AdamW.
+// ---------------------------------------------------------------------------
+namespace seqattn {
+namespace {
+
+// 2-D bf16 tensor map over a row-major [rows, cols] matrix with a row stride
+// of `ld` elements: box {64 columns, box_rows rows}, 128-byte swizzle; reads
+// past the matrix give zeros.
+bool make_map_2d(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  memset(m, 0, sizeof(*m));
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+seqattn_status check_ld(int64_t ld, int64_t cols, const char* name) {
+  if (ld < cols || ld % 8 != 0 || ld > (int64_t{1} << 36))
+    return fail(SEQATTN_ERR_INVALID_ARG, "row stride of %s (%lld) must be a multiple of 8 and at least %lld", name,
+                (long long)ld, (long long)cols);
+  return SEQATTN_OK;
+}
+
+seqattn_status check_linear(int64_t rows, int32_t k, int32_t n, int32_t act) {
+  if (rows < 0 || rows >= INT32_MAX - 511)
+    return fail(SEQATTN_ERR_INVALID_ARG, "rows (%lld) must lie in [0, 2^31 - 512)", (long long)rows);
+  if (k < 8 || k % 8 || n < 8 || n % 8 || k > INT32_MAX - 511 || n > INT32_MAX - 511)
+    return fail(SEQATTN_ERR_INVALID_ARG, "k (%d) and n (%d) must be positive multiples of 8", k, n);
+  if (act < SEQATTN_ACT_NONE || act > SEQATTN_ACT_GELU_TANH)
+    return fail(SEQATTN_ERR_INVALID_ARG, "unknown activation %d", act);
+  return SEQATTN_OK;
+}
+
+// Common end of the three linear calls: error word, wait limit, maps, launch.
+// Operand a carries the result's row index, b its column index; a tile of an
+// operand whose contiguous dimension is that index (MN-major) is a stage of
+// contraction rows high, of the other kind (K-major) 128 index rows.
+seqattn_status run_linear(int mode, LinearParams& p, const void* a, int64_t lda, const void* b, int64_t ldb,
+                          seqattn_stream_t stream) {
+  unsigned int* err = nullptr;
+  cudaError_t e = error_word(&err);
+  if (e != cudaSuccess) return cuda_fail(e, "error word");
+  p.err = err;
+  p.wait_cycles = g_wait_cycles.load(std::memory_order_relaxed);
+  const bool a_mn = mode == kLinearWgrad, b_mn = mode != kLinearDgrad;
+  LinearMaps maps;
+  const bool made = (a_mn ? make_map_2d(&maps.a, a, p.k, p.m, lda, kLinearStageK)
+                        : make_map_2d(&maps.a, a, p.m, p.k, lda, 128)) &&
+                  (b_mn ? make_map_2d(&maps.b, b, p.k, p.n, ldb, kLinearStageK)
+                        : make_map_2d(&maps.b, b, p.n, p.k, ldb, 128));
+  if (!made) return fail(SEQATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed for the operands of the product");
+  e = launch_linear_bf16(mode, maps, p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "linear launch");
+}
+
+}  // namespace
+}  // namespace seqattn
+
+extern "C" {
+
+seqattn_status seqattn_linear_fwd(int64_t rows, int32_t k, int32_t n, const void* x, int64_t ldx, const void* w,
+                                  const void* bias, int32_t act, const void* residual, int64_t ldr, void* z,
+                                  int64_t ldz, void* y, int64_t ldy, seqattn_stream_t stream) {
+  seqattn_status s = check_linear(rows, k, n, act);
+  if (s != SEQATTN_OK) return s;
+  if ((s = check_ld(ldx, k, "x")) != SEQATTN_OK || (s = check_ld(ldy, n, "y")) != SEQATTN_OK) return s;
+  if (residual != nullptr && (s = check_ld(ldr, n, "residual")) != SEQATTN_OK) return s;
+  if (z != nullptr && (s = check_ld(ldz, n, "z")) != SEQATTN_OK) return s;
+  if (rows == 0) return ok();
+  s = check_ptrs({{x, "x"}, {w, "w"}, {y, "y"}});
+  if (s != SEQATTN_OK) return s;
+  if (!aligned16(bias) || !aligned16(residual) || !aligned16(z))
+    return fail(SEQATTN_ERR_INVALID_ARG, "bias, residual or z is not 16-byte aligned");
+  LinearParams p = {};
+  p.m = static_cast<int>(rows);
+  p.n = n;
+  p.k = k;
+  p.act = act;
+  p.bias = static_cast<const __nv_bfloat16*>(bias);
+  p.residual = static_cast<const __nv_bfloat16*>(residual);
+  p.z = static_cast<__nv_bfloat16*>(z);
+  p.out = y;
+  p.ldr = ldr;
+  p.ldz = ldz;
+  p.ldo = ldy;
+  return run_linear(kLinearFwd, p, x, ldx, w, n, stream);
+}
+
+seqattn_status seqattn_linear_dgrad(int64_t rows, int32_t k, int32_t n, const void* g, int64_t ldg, const void* w,
+                                    int32_t act, const void* z, int64_t ldz, const void* residual, int64_t ldr,
+                                    void* dx, int64_t lddx, seqattn_stream_t stream) {
+  seqattn_status s = check_linear(rows, k, n, act);
+  if (s != SEQATTN_OK) return s;
+  if ((s = check_ld(ldg, n, "g")) != SEQATTN_OK || (s = check_ld(lddx, k, "dx")) != SEQATTN_OK) return s;
+  if (residual != nullptr && (s = check_ld(ldr, k, "residual")) != SEQATTN_OK) return s;
+  if (act != SEQATTN_ACT_NONE) {
+    if (z == nullptr && rows > 0) return fail(SEQATTN_ERR_INVALID_ARG, "z is NULL but act is not NONE");
+    if ((s = check_ld(ldz, k, "z")) != SEQATTN_OK) return s;
+  }
+  if (rows == 0) return ok();
+  s = check_ptrs({{g, "g"}, {w, "w"}, {dx, "dx"}});
+  if (s != SEQATTN_OK) return s;
+  if (!aligned16(residual) || !aligned16(z))
+    return fail(SEQATTN_ERR_INVALID_ARG, "residual or z is not 16-byte aligned");
+  LinearParams p = {};
+  p.m = static_cast<int>(rows);
+  p.n = k;
+  p.k = n;
+  p.act = act;
+  p.residual = static_cast<const __nv_bfloat16*>(residual);
+  p.z = static_cast<__nv_bfloat16*>(const_cast<void*>(z));   // read only by dgrad
+  p.out = dx;
+  p.ldr = ldr;
+  p.ldz = ldz;
+  p.ldo = lddx;
+  return run_linear(kLinearDgrad, p, g, ldg, w, n, stream);
+}
+
+seqattn_status seqattn_linear_wgrad(int64_t rows, int32_t k, int32_t n, const void* x, int64_t ldx, const void* g,
+                                    int64_t ldg, float* dw, float* dbias, seqattn_stream_t stream) {
+  seqattn_status s = check_linear(rows, k, n, SEQATTN_ACT_NONE);
+  if (s != SEQATTN_OK) return s;
+  if ((s = check_ld(ldx, k, "x")) != SEQATTN_OK || (s = check_ld(ldg, n, "g")) != SEQATTN_OK) return s;
+  if (rows == 0) return ok();
+  s = check_ptrs({{x, "x"}, {g, "g"}, {dw, "dw"}});
+  if (s != SEQATTN_OK) return s;
+  if (!aligned16(dbias)) return fail(SEQATTN_ERR_INVALID_ARG, "dbias is not 16-byte aligned");
+  LinearParams p = {};
+  p.m = k;
+  p.n = n;
+  p.k = static_cast<int>(rows);
+  p.out = dw;
+  p.ldo = n;
+  s = run_linear(kLinearWgrad, p, x, ldx, g, ldg, stream);
+  if (s != SEQATTN_OK || dbias == nullptr) return s;
+  const cudaError_t e =
+      launch_colsum_bf16(g, ldg, static_cast<int>(rows), n, dbias, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "column sum launch");
+}
+
+}  // extern "C"
+
+namespace seqattn {
+namespace {
+
+// The checks that the forward and the backward of the head norm share, and
+// the part of the launch parameters that they fill.
+seqattn_status check_norm_rope(const seqattn_problem* pb, int64_t q_start, int64_t q_len, const void* gamma_q,
+                               const void* gamma_k, float eps, const seqattn_rope_plan* plan,
+                               const int64_t* positions, NormRopeParams* p) {
+  seqattn_status s = check_problem(pb);
+  if (s != SEQATTN_OK) return s;
+  if (q_start < 0 || q_len < 0 || q_start + q_len > pb->seq_capacity)
+    return fail(SEQATTN_ERR_INVALID_ARG, "need 0 <= q_start and 0 <= q_len and q_start + q_len <= seq_capacity (got %lld, %lld)",
+                (long long)q_start, (long long)q_len);
+  if ((gamma_q == nullptr) != (gamma_k == nullptr))
+    return fail(SEQATTN_ERR_INVALID_ARG, "gamma_q and gamma_k must both be given or both be NULL");
+  if (gamma_q != nullptr && !(eps >= 0.f && isfinite(eps)))
+    return fail(SEQATTN_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!aligned16(gamma_q) || !aligned16(gamma_k))
+    return fail(SEQATTN_ERR_INVALID_ARG, "gamma is not 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(positions) & 7u) != 0)
+    return fail(SEQATTN_ERR_INVALID_ARG, "positions is not 8-byte aligned");
+  p->B = pb->batch;
+  p->q_len = static_cast<int>(q_len);
+  p->Hq = pb->num_q_heads;
+  p->Hkv = pb->num_kv_heads;
+  p->T = pb->seq_capacity;
+  p->q_start = q_start;
+  p->gamma_q = gamma_q;
+  p->gamma_k = gamma_k;
+  p->eps = eps;
+  p->positions = positions;
+  p->rot_dim = 0;
+  if (plan != nullptr) {
+    if (plan->rot_dim < 16 || plan->rot_dim % 16 || plan->rot_dim > pb->head_dim)
+      return fail(SEQATTN_ERR_INVALID_ARG, "rot_dim %d is not a multiple of 16 in [16, head_dim]", plan->rot_dim);
+    if (plan->axes < 1 || plan->axes > 64 || (plan->interleaved != 0 && plan->interleaved != 1) ||
+        plan->reserved != 0)
+      return fail(SEQATTN_ERR_INVALID_ARG, "rope plan: axes must lie in [1, 64], interleaved be 0 or 1, reserved 0");
+    for (int i = 0; i < plan->rot_dim / 2; ++i)
+      if (plan->axis[i] >= plan->axes)
+        return fail(SEQATTN_ERR_INVALID_ARG, "rope plan: axis[%d] = %d is not below axes = %d", i, plan->axis[i],
+                    plan->axes);
+    p->rot_dim = plan->rot_dim;
+    p->axes = plan->axes;
+    p->interleaved = plan->interleaved;
+    memcpy(p->turns, plan->turns, sizeof(p->turns));
+    memcpy(p->axis, plan->axis, sizeof(p->axis));
+  }
+  return SEQATTN_OK;
+}
+
+size_t norm_rope_workspace(int head_dim) {
+  return static_cast<size_t>(norm_rope_bwd_blocks()) * 2 * head_dim * sizeof(float);
+}
+
+}  // namespace
+}  // namespace seqattn
+
+extern "C" {
+
+seqattn_status seqattn_qk_norm_rope_fwd(const seqattn_problem* pb, int64_t q_start, int64_t q_len, const void* q_in,
+                                        int64_t ld_q, const void* k_in, int64_t ld_k, const void* v_in, int64_t ld_v,
+                                        const void* gamma_q, const void* gamma_k, float eps,
+                                        const seqattn_rope_plan* plan, const int64_t* positions, void* q,
+                                        void* k_cache, void* v_cache, seqattn_stream_t stream) {
+  NormRopeParams p = {};
+  seqattn_status s = check_norm_rope(pb, q_start, q_len, gamma_q, gamma_k, eps, plan, positions, &p);
+  if (s != SEQATTN_OK) return s;
+  const int64_t nq = static_cast<int64_t>(pb->num_q_heads) * pb->head_dim;
+  const int64_t nk = static_cast<int64_t>(pb->num_kv_heads) * pb->head_dim;
+  if ((v_in == nullptr) != (v_cache == nullptr))
+    return fail(SEQATTN_ERR_INVALID_ARG, "v_in and v_cache must both be given or both be NULL");
+  if ((s = check_ld(ld_q, nq, "q_in")) != SEQATTN_OK || (s = check_ld(ld_k, nk, "k_in")) != SEQATTN_OK) return s;
+  if (v_in != nullptr && (s = check_ld(ld_v, nk, "v_in")) != SEQATTN_OK) return s;
+  if (q_len == 0) return ok();
+  s = check_ptrs({{q_in, "q_in"}, {k_in, "k_in"}, {q, "q"}, {k_cache, "k_cache"}});
+  if (s != SEQATTN_OK) return s;
+  if (!aligned16(v_in) || !aligned16(v_cache))
+    return fail(SEQATTN_ERR_INVALID_ARG, "v_in or v_cache is not 16-byte aligned");
+  p.q_in = q_in;
+  p.k_in = k_in;
+  p.v_in = v_in;
+  p.q_stride = ld_q;
+  p.k_stride = ld_k;
+  p.v_stride = ld_v;
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  const cudaError_t e = launch_norm_rope_fwd(p, pb->head_dim, pb->dtype == SEQATTN_BF16,
+                                             reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "norm_rope_fwd launch");
+}
+
+size_t seqattn_qk_norm_rope_bwd_workspace_size(const seqattn_problem* pb) {
+  return check_problem(pb) == SEQATTN_OK ? norm_rope_workspace(pb->head_dim) : 0;
+}
+
+seqattn_status seqattn_qk_norm_rope_bwd(const seqattn_problem* pb, int64_t q_start, int64_t q_len, const void* q_in,
+                                        int64_t ld_q, const void* k_in, int64_t ld_k, const void* gamma_q,
+                                        const void* gamma_k, float eps, const seqattn_rope_plan* plan,
+                                        const int64_t* positions, const float* dq, const float* dk_accum,
+                                        const float* dv_accum, void* dq_in, int64_t ld_dq, void* dk_in,
+                                        int64_t ld_dk, void* dv_in, int64_t ld_dv, float* dgamma_q, float* dgamma_k,
+                                        void* workspace, size_t workspace_size, seqattn_stream_t stream) {
+  NormRopeParams p = {};
+  seqattn_status s = check_norm_rope(pb, q_start, q_len, gamma_q, gamma_k, eps, plan, positions, &p);
+  if (s != SEQATTN_OK) return s;
+  const int64_t nq = static_cast<int64_t>(pb->num_q_heads) * pb->head_dim;
+  const int64_t nk = static_cast<int64_t>(pb->num_kv_heads) * pb->head_dim;
+  const bool norm = gamma_q != nullptr;
+  if ((dv_accum == nullptr) != (dv_in == nullptr))
+    return fail(SEQATTN_ERR_INVALID_ARG, "dv_accum and dv_in must both be given or both be NULL");
+  if ((s = check_ld(ld_dq, nq, "dq_in")) != SEQATTN_OK || (s = check_ld(ld_dk, nk, "dk_in")) != SEQATTN_OK) return s;
+  if (dv_in != nullptr && (s = check_ld(ld_dv, nk, "dv_in")) != SEQATTN_OK) return s;
+  if (norm && ((s = check_ld(ld_q, nq, "q_in")) != SEQATTN_OK || (s = check_ld(ld_k, nk, "k_in")) != SEQATTN_OK))
+    return s;
+  if (q_len == 0) return ok();
+  s = check_ptrs({{dq, "dq"}, {dk_accum, "dk_accum"}, {dq_in, "dq_in"}, {dk_in, "dk_in"}});
+  if (s != SEQATTN_OK) return s;
+  if (!aligned16(dv_accum) || !aligned16(dv_in))
+    return fail(SEQATTN_ERR_INVALID_ARG, "dv_accum or dv_in is not 16-byte aligned");
+  if (norm) {
+    s = check_ptrs({{q_in, "q_in"}, {k_in, "k_in"}, {dgamma_q, "dgamma_q"}, {dgamma_k, "dgamma_k"},
+                    {workspace, "workspace"}});
+    if (s != SEQATTN_OK) return s;
+    if (workspace_size < norm_rope_workspace(pb->head_dim))
+      return fail(SEQATTN_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed", workspace_size,
+                  norm_rope_workspace(pb->head_dim));
+    p.q_in = q_in;
+    p.k_in = k_in;
+    p.q_stride = ld_q;
+    p.k_stride = ld_k;
+    p.dgamma_q = dgamma_q;
+    p.dgamma_k = dgamma_k;
+    p.partial = static_cast<float*>(workspace);
+  }
+  p.dq = dq;
+  p.dk = dk_accum;
+  p.dv = dv_accum;
+  p.dq_in = dq_in;
+  p.dk_in = dk_in;
+  p.dv_in = dv_in;
+  p.dq_stride = ld_dq;
+  p.dk_stride = ld_dk;
+  p.dv_stride = ld_dv;
+  const cudaError_t e = launch_norm_rope_bwd(p, pb->head_dim, pb->dtype == SEQATTN_BF16,
+                                             reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "norm_rope_bwd launch");
+}
+
+static_assert(sizeof(seqattn_adamw_tensor) == sizeof(AdamwTensor), "the internal descriptor mirrors the public one");
+
+seqattn_status seqattn_adamw_step(const seqattn_adamw_tensor* tensors, int32_t count, int32_t state_bits,
+                                  const seqattn_adamw_params* params, seqattn_stream_t stream) {
+  if (count < 0 || (count > 0 && tensors == nullptr) || params == nullptr)
+    return fail(SEQATTN_ERR_INVALID_ARG, "tensors or params is NULL, or count (%d) < 0", count);
+  if (state_bits != 8 && state_bits != 32)
+    return fail(SEQATTN_ERR_INVALID_ARG, "state_bits %d is not 8 or 32", state_bits);
+  const seqattn_adamw_params& a = *params;
+  if (!(a.beta1 >= 0 && a.beta1 < 1 && a.beta2 >= 0 && a.beta2 < 1))
+    return fail(SEQATTN_ERR_INVALID_ARG, "beta1 and beta2 must lie in [0, 1)");
+  if (!isfinite(a.lr) || !isfinite(a.grad_scale) || !(a.eps >= 0 && isfinite(a.eps)))
+    return fail(SEQATTN_ERR_INVALID_ARG, "lr and grad_scale must be finite, eps finite and >= 0");
+  if (a.step < 1 && a.step_dev == nullptr)
+    return fail(SEQATTN_ERR_INVALID_ARG, "step %lld < 1", (long long)a.step);
+  if ((reinterpret_cast<uintptr_t>(a.lr_dev) & 3u) || (reinterpret_cast<uintptr_t>(a.grad_scale_dev) & 3u) ||
+      (reinterpret_cast<uintptr_t>(a.step_dev) & 7u))
+    return fail(SEQATTN_ERR_INVALID_ARG, "lr_dev, grad_scale_dev or step_dev is misaligned");
+  for (int32_t i = 0; i < count; ++i) {
+    const seqattn_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.n > (int64_t{1} << 40))
+      return fail(SEQATTN_ERR_INVALID_ARG, "tensor %d: n = %lld", i, (long long)t.n);
+    if (!isfinite(t.weight_decay) || (t.grad_bf16 != 0 && t.grad_bf16 != 1))
+      return fail(SEQATTN_ERR_INVALID_ARG, "tensor %d: weight_decay must be finite and grad_bf16 0 or 1", i);
+    if (t.n == 0) continue;
+    seqattn_status s = check_ptrs({{t.param, "param"}, {t.grad, "grad"}, {t.m, "m"}, {t.v, "v"}});
+    if (s != SEQATTN_OK) return s;
+    if (!aligned16(t.lowp)) return fail(SEQATTN_ERR_INVALID_ARG, "tensor %d: lowp is not 16-byte aligned", i);
+    if (state_bits == 8 && (t.m_scale == nullptr || t.v_scale == nullptr ||
+                            (reinterpret_cast<uintptr_t>(t.m_scale) & 3u) || (reinterpret_cast<uintptr_t>(t.v_scale) & 3u)))
+      return fail(SEQATTN_ERR_INVALID_ARG, "tensor %d: m_scale or v_scale is NULL or not 4-byte aligned", i);
+  }
+  AdamwHyper h = {};
+  h.lr = static_cast<float>(a.lr);
+  h.beta1 = static_cast<float>(a.beta1);
+  h.one_minus_beta1 = static_cast<float>(1.0 - a.beta1);
+  h.beta2 = static_cast<float>(a.beta2);
+  h.one_minus_beta2 = static_cast<float>(1.0 - a.beta2);
+  h.eps = static_cast<float>(a.eps);
+  h.grad_scale = static_cast<float>(a.grad_scale);
+  if (a.step_dev == nullptr) {
+    h.step_size = static_cast<float>(a.lr / (1.0 - pow(a.beta1, static_cast<double>(a.step))));
+    h.inv_root_bc2 = 1.f / static_cast<float>(sqrt(1.0 - pow(a.beta2, static_cast<double>(a.step))));
+  }
+  h.lrd = a.lr;
+  h.beta1d = a.beta1;
+  h.beta2d = a.beta2;
+  h.step = a.step;
+  h.lr_dev = a.lr_dev;
+  h.grad_scale_dev = a.grad_scale_dev;
+  h.step_dev = a.step_dev;
+  const cudaError_t e = launch_adamw(reinterpret_cast<const AdamwTensor*>(tensors), count, state_bits, h,
+                                     reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "adamw launch");
+}
+
+}  // extern "C"
