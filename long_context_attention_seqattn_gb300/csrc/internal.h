@@ -89,6 +89,8 @@ struct LinearParams {
   __nv_bfloat16* z;            // pre-activation: written by the forward, read by dgrad
   void* out;                   // bf16 (forward, dgrad) or float32 accumulator (wgrad)
   int64_t ldr, ldz, ldo;       // row strides in elements
+  int split;                   // CTAs that share a tile (split shape)
+  uint32_t a_bytes;            // bytes of one A tile's copies (split shape)
   unsigned int* err;
   long long wait_cycles;
 };

@@ -13,12 +13,34 @@
 //   wgrad     X^T k,    MN-major   G   n,   MN-major   rows
 // Rows, columns and contraction tails past the tensors arrive as TMA zeros.
 //
-// One CTA owns a 128 x 128 tile of the result and streams the contraction in
-// stages of 64 through a shared-memory ring:
+// Two shapes of the kernel:
+//   pair   clusters of two CTAs, persistent.  A pair owns a 256 x 256 tile:
+//          one thread issues M256 N256 K16 MMAs for both SMs, each SM loads
+//          half of A (its 128 rows) and half of B (128 columns), 32 KB a stage
+//          of 64, and keeps its 128 x 256 half of the result in TMEM.  Two
+//          result buffers (512 columns): the epilogue of a tile runs under
+//          the products of the next.
+//   split  clusters of 1 to 8 CTAs that share one 128 x 128 tile: CTA i sums
+//          the i-th part of the contraction, the parts meet in distributed
+//          shared memory and are added in order.  For results with few tiles
+//          (few rows, down to a single token's, or a small weight gradient),
+//          where the pairs would leave most SMs idle.
+// Warps of a CTA:
 //   warp 0      TMA producer (A and B tile of a stage, 16 KB each)
-//   warp 1      TMEM owner + MMA issuer (4 MMAs M128 N128 K16 per stage)
-//   warps 2..5  epilogue, one TMEM lane quadrant each: a thread owns one row
+//   warp 1      TMEM owner + MMA issuer (pair: the even CTA's thread for both)
+//   warps 2..9  epilogue, two per TMEM lane quadrant, each half of the columns
+//               of its 32 rows
+//
+// wgrad's result is float32, and a long running sum on the tensor core is not
+// quite: its additions truncate (measured: 9.1e-6 relative over 8192 rows,
+// against 9.5e-7 for a float32 library product).  So its products are summed
+// in TMEM for at most kChunkStages stages (512 rows); the epilogue warps add
+// these partial sums in registers, rounding to nearest, while the next are
+// computed into the other buffer.  bf16 results need no such care.
 #include <cuda_bf16.h>
+
+#include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "sm103_ptx.cuh"
@@ -26,20 +48,35 @@
 namespace seqattn {
 namespace {
 
-constexpr int kTM = 128;                       // result rows per CTA
-constexpr int kTN = 128;                       // result columns per CTA
 constexpr int kTK = kLinearStageK;             // contraction per stage
+constexpr int kOperandRows = 128;              // rows of an operand tile in one CTA
 constexpr int kStages = 6;
-constexpr int kOperandBytes = kTM * kTK * 2;   // 16 KB, either operand
+constexpr int kOperandBytes = kOperandRows * kTK * 2;   // 16 KB, either operand
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMnBlockBytes = kTK * 128;       // one 64-column block of an MN-major tile
-constexpr int kThreads = 192;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kSmemAlloc = kStages * kStageBytes + 1024;
-constexpr uint32_t kTmemCols = 128;
+constexpr int kChunkStages = 8;                // wgrad: stages summed on the tensor core
+constexpr int kMaxSplit = 8;                   // CTAs of a split cluster (portable limit)
+constexpr int kPartStride = 128 + 4;           // floats between rows of a split CTA's partial tile
+// Cost model of the two shapes, in SM cycles (see launch_mode).
+constexpr int64_t kPairStageCost = 600, kPairFixedCost = 6000;
+constexpr int64_t kSplitStageCost = 500, kSplitFixedCost = 6000;
+static_assert(128 * kPartStride * 4 <= kStages * kStageBytes, "the partial tile is kept in the ring");
+
+template <bool kPair>
+struct Shape {
+  static constexpr int kCtas = kPair ? 2 : 1;
+  static constexpr int kTM = 128 * kCtas;      // tile rows
+  static constexpr int kTN = 128 * kCtas;      // tile columns
+  static constexpr uint32_t kTmemCols = 2 * kTN;   // two result buffers
+  static constexpr int kColsPerWarp = kTN / 2;
+};
 
 struct LinearBarriers {
   uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full;
+  uint64_t acc_full[2], acc_empty[2];
   uint64_t mma_final;
 };
 
@@ -92,10 +129,17 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-// Eight consecutive columns of one result row, forward or dgrad.
+// Eight consecutive columns of one result row.
 template <int kMode, int kAct>
 __device__ __forceinline__ void finish8(const LinearParams& p, int64_t row, int col, float (&v)[8]) {
   float t[8];
+  if constexpr (kMode == kLinearWgrad) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.ldo + col);
+    const float4 a = o[0], b = o[1];
+    o[0] = make_float4(a.x + v[0], a.y + v[1], a.z + v[2], a.w + v[3]);
+    o[1] = make_float4(b.x + v[4], b.y + v[5], b.z + v[6], b.w + v[7]);
+    return;
+  }
   if constexpr (kMode == kLinearFwd) {
     if (p.bias != nullptr) {
       unpack8(__ldg(reinterpret_cast<const uint4*>(p.bias + col)), t);
@@ -118,15 +162,31 @@ __device__ __forceinline__ void finish8(const LinearParams& p, int64_t row, int 
   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * p.ldo + col) = pack8(v);
 }
 
+// 32 consecutive columns of one row (as many as the result has).
 template <int kMode, int kAct>
-__device__ __forceinline__ void finish32(const LinearParams& p, int64_t row, int col, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void finish32(const LinearParams& p, int64_t row, int col, const float (&r)[32]) {
 #pragma unroll
   for (int j = 0; j < 32; j += 8) {
     if (col + j >= p.n) break;
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[j + i]);
+    for (int i = 0; i < 8; ++i) v[i] = r[j + i];
     finish8<kMode, kAct>(p, row, col + j, v);
+  }
+}
+
+template <int kMode, typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  if constexpr (kMode == kLinearWgrad) {
+    f(std::integral_constant<int, kActNone>());
+  } else {
+    switch (act) {
+      case kActRelu: f(std::integral_constant<int, kActRelu>()); break;
+      case kActSilu: f(std::integral_constant<int, kActSilu>()); break;
+      case kActGelu: f(std::integral_constant<int, kActGelu>()); break;
+      case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>()); break;
+      default: f(std::integral_constant<int, kActNone>()); break;
+    }
   }
 }
 
@@ -143,134 +203,257 @@ __host__ __device__ constexpr uint32_t kstep_off(int ks) {
 }
 
 // One operand tile: 128 of its M/N index at `mn`, 64 of the contraction at `k`.
-template <bool kMn>
-__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int mn, int k) {
-  if constexpr (kMn) {
-    tma_load_2d(dst, map, bar, mn, k);
-    tma_load_2d(dst + kMnBlockBytes, map, bar, mn + 64, k);
+template <bool kMn, bool kPair>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, uint32_t pair_bar,
+                                          int mn, int k) {
+  if constexpr (kPair) {
+    if constexpr (kMn) {
+      tma_load_2d_pair(dst, map, pair_bar, mn, k);
+      tma_load_2d_pair(dst + kMnBlockBytes, map, pair_bar, mn + 64, k);
+    } else {
+      tma_load_2d_pair(dst, map, pair_bar, k, mn);
+    }
   } else {
-    tma_load_2d(dst, map, bar, k, mn);
+    if constexpr (kMn) {
+      tma_load_2d(dst, map, bar, mn, k);
+      tma_load_2d(dst + kMnBlockBytes, map, bar, mn + 64, k);
+    } else {
+      tma_load_2d(dst, map, bar, k, mn);
+    }
   }
 }
 
-template <int kMode>
+// Tile t of the result.  Bands of 8 tile rows, rows fastest within a band:
+// the tiles in flight form a block of the result, whose operands L2 serves.
+struct Tiles {
+  int m, n;
+  __device__ __forceinline__ void at(int t, int* tm, int* tn) const {
+    const int band = 8 * n;
+    const int b = t / band, r = t - b * band;
+    const int rows = min(8, m - 8 * b);
+    *tm = 8 * b + r % rows;
+    *tn = r / rows;
+  }
+};
+
+template <int kMode, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_bf16_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                        const __grid_constant__ LinearParams p) {
+  using S = Shape<kPair>;
   constexpr bool kAMn = kMode == kLinearWgrad;
   constexpr bool kBMn = kMode != kLinearDgrad;
-  if (error_already_set(p.err)) return;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   __shared__ LinearBarriers bars;
   __shared__ uint32_t tmem_base_sh;
+  __shared__ uint32_t skip_sh;
   __shared__ int abort_flag;
   Watchdog wd(&abort_flag, p.err, p.wait_cycles);
 
-  const int m_tiles = (p.m + kTM - 1) / kTM;
-  const int m0 = (blockIdx.x % m_tiles) * kTM;
-  const int n0 = (blockIdx.x / m_tiles) * kTN;
-  const int n_st = (p.k + kTK - 1) / kTK;
-
+  const uint32_t rank = cluster_rank();
   const int warp = warp_id();
   const int lane = lane_id();
   if (threadIdx.x == 0) {
     abort_flag = 0;
+    skip_sh = error_already_set(p.err) ? 1u : 0u;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars.full[i], 1);
       mbar_init(&bars.empty[i], 1);
     }
-    mbar_init(&bars.acc_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.acc_full[i], 1);
+      mbar_init(&bars.acc_empty[i], kEpiWarps * S::kCtas);
+    }
     mbar_init(&bars.mma_final, 1);
     fence_barrier_init();
   }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&map_a);
+    prefetch_tensormap(&map_b);
+  }
   if (warp == 1) {
-    tmem_alloc(&tmem_base_sh, kTmemCols);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem_alloc_pair(&tmem_base_sh, S::kTmemCols);
+    } else {
+      tmem_alloc(&tmem_base_sh, S::kTmemCols);
+      tmem_relinquish();
+    }
   }
   __syncthreads();
+  cluster_sync();          // barriers of every CTA of the cluster are ready
   tc_fence_after_sync();
   const uint32_t tmem = tmem_base_sh;
+  // one decision for the cluster, so that no CTA waits for one that left
+  const bool skip = ld_cluster_u32(cluster_map(smem_u32(&skip_sh), 0)) != 0u;
+
+  // ---- this cluster's tiles and this CTA's part of the contraction
+  const Tiles tiles = {(p.m + S::kTM - 1) / S::kTM, (p.n + S::kTN - 1) / S::kTN};
+  const int all_stages = (p.k + kTK - 1) / kTK;
+  const int ctas = kPair ? 2 : p.split;
+  const int first_tile = blockIdx.x / ctas;
+  const int tile_step = gridDim.x / ctas;
+  const int n_tiles = tiles.m * tiles.n;
+  // split: parts of the contraction as even as whole stages allow
+  const int s_begin = kPair ? 0 : static_cast<int>(static_cast<int64_t>(all_stages) * rank / ctas);
+  const int s_end = kPair ? all_stages : static_cast<int>(static_cast<int64_t>(all_stages) * (rank + 1) / ctas);
+  const int n_st = s_end - s_begin;
+  const int chunk = kMode == kLinearWgrad ? kChunkStages : n_st;   // stages of one result buffer
   int n_issued = 0;
 
-  if (warp == 0) {
+  if (skip) {
+    // leave together below
+  } else if (warp == 0) {
     if (lane == 0) {
-      prefetch_tensormap(&map_a);
-      prefetch_tensormap(&map_b);
-      for (int s = 0; s < n_st; ++s) {
-        const int st = s % kStages;
-        if (!wd.wait_sleep(&bars.empty[st], ((s / kStages) & 1) ^ 1)) break;
-        uint8_t* stage = smem + st * kStageBytes;
-        mbar_arrive_expect_tx(&bars.full[st], kStageBytes);
-        load_tile<kAMn>(stage, &map_a, &bars.full[st], m0, s * kTK);
-        load_tile<kBMn>(stage + kOperandBytes, &map_b, &bars.full[st], n0, s * kTK);
-        n_issued = s + 1;
+      int it = 0;
+      bool ok = true;
+      for (int t = first_tile; ok && t < n_tiles; t += tile_step) {
+        int tm, tn;
+        tiles.at(t, &tm, &tn);
+        const int m0 = tm * S::kTM + (kPair ? 128 * static_cast<int>(rank) : 0);
+        const int n0 = tn * S::kTN + (kPair ? 128 * static_cast<int>(rank) : 0);
+        for (int s = s_begin; s < s_end; ++s, ++it) {
+          const int st = it % kStages;
+          if (!(ok = wd.wait_sleep(&bars.empty[st], ((it / kStages) & 1) ^ 1))) break;
+          uint8_t* stage = smem + st * kStageBytes;
+          uint32_t pair_bar = 0;
+          if constexpr (kPair) {
+            // both CTAs' copies count on the even CTA's barrier, which its
+            // producer arms with the bytes of both
+            pair_bar = cluster_map(smem_u32(&bars.full[st]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], 2 * kStageBytes);
+          } else {
+            mbar_arrive_expect_tx(&bars.full[st], p.a_bytes + kOperandBytes);
+          }
+          load_tile<kAMn, kPair>(stage, &map_a, &bars.full[st], pair_bar, m0, s * kTK);
+          load_tile<kBMn, kPair>(stage + kOperandBytes, &map_b, &bars.full[st], pair_bar, n0, s * kTK);
+          n_issued = it + 1;
+        }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = make_idesc_bf16(kTM, kTN, kAMn, kBMn);
+    if (lane == 0 && (!kPair || rank == 0)) {
+      const uint32_t idesc = make_idesc_bf16(S::kTM, S::kTN, kAMn, kBMn);
       const uint64_t a0 = make_desc_sw128(smem_u32(smem), kAMn ? kMnBlockBytes : 16, 1024);
       const uint64_t b0 = make_desc_sw128(smem_u32(smem) + kOperandBytes, kBMn ? kMnBlockBytes : 16, 1024);
+      int it = 0, c = 0;       // stages and result buffers issued so far
       bool ok = true;
-      for (int s = 0; s < n_st; ++s) {
-        const int st = s % kStages;
-        if (!(ok = wd.wait_sleep(&bars.full[st], (s / kStages) & 1))) break;
-        tc_fence_after_sync();
-        const uint64_t off = static_cast<uint64_t>(st * (kStageBytes >> 4));
+      for (int t = first_tile; ok && t < n_tiles; t += tile_step) {
+        for (int s = 0; ok && s < n_st; ++c) {
+          if (!(ok = wd.wait_sleep(&bars.acc_empty[c & 1], ((c >> 1) & 1) ^ 1))) break;
+          tc_fence_after_sync();
+          const uint32_t d = tmem + static_cast<uint32_t>((c & 1) * S::kTN);
+          const int s_chunk = min(n_st, s + chunk);
+          for (bool first = true; s < s_chunk; ++s, ++it) {
+            const int st = it % kStages;
+            if (!(ok = wd.wait_sleep(&bars.full[st], (it / kStages) & 1))) break;
+            tc_fence_after_sync();
+            const uint64_t off = static_cast<uint64_t>(st * (kStageBytes >> 4));
 #pragma unroll
-        for (int ks = 0; ks < kTK / 16; ++ks)
-          umma_bf16_ss(tmem, a0 + off + kstep_off<kAMn>(ks), b0 + off + kstep_off<kBMn>(ks), idesc,
-                       (s > 0 || ks > 0) ? 1u : 0u);
-        umma_commit(&bars.empty[st]);
+            for (int ks = 0; ks < kTK / 16; ++ks) {
+              const uint64_t a = a0 + off + kstep_off<kAMn>(ks), b = b0 + off + kstep_off<kBMn>(ks);
+              const uint32_t add = (first && ks == 0) ? 0u : 1u;
+              if constexpr (kPair) umma_bf16_ss_pair(d, a, b, idesc, add);
+              else umma_bf16_ss(d, a, b, idesc, add);
+            }
+            first = false;
+            if constexpr (kPair) umma_commit_pair(&bars.empty[st]);
+            else umma_commit(&bars.empty[st]);
+          }
+          if (!ok) break;
+          if constexpr (kPair) umma_commit_pair(&bars.acc_full[c & 1]);
+          else umma_commit(&bars.acc_full[c & 1]);
+        }
       }
-      if (ok) umma_commit(&bars.acc_full);
-      umma_commit(&bars.mma_final);
+      if constexpr (kPair) umma_commit_pair(&bars.mma_final);
+      else umma_commit(&bars.mma_final);
       wd.drain(&bars.mma_final, 0, 4000000);
     }
   } else {
+    // ---------------------------------------------------------------- epilogue
     const int quad = warp & 3;
+    const int half = (warp - 2) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-    const int64_t row = m0 + quad * 32 + lane;
-    if (warp_wait(wd, &bars.acc_full, 0)) {
-      tc_fence_after_sync();
-#pragma unroll 1
-      for (int c0 = 0; c0 < kTN && n0 + c0 < p.n; c0 += 32) {
-        uint32_t r[32];
-        tmem_ld32(tmem + lane_base + c0, r);
-        tmem_ld_wait();
-        if (row >= p.m) continue;
-        if constexpr (kMode == kLinearWgrad) {
-          float* o = static_cast<float*>(p.out) + row * p.ldo + n0 + c0;
+    const uint32_t my_cols = tmem + lane_base + static_cast<uint32_t>(half * S::kColsPerWarp);
+    const int tile_row = (kPair ? 128 * static_cast<int>(rank) : 0) + quad * 32 + lane;
+    const uint32_t leader_empty[2] = {cluster_map(smem_u32(&bars.acc_empty[0]), kPair ? 0 : rank),
+                                      cluster_map(smem_u32(&bars.acc_empty[1]), kPair ? 0 : rank)};
+    int c = 0;
+    bool ok = true;
+    for (int t = first_tile; ok && t < n_tiles; t += tile_step) {
+      int tm, tn;
+      tiles.at(t, &tm, &tn);
+      const int64_t row = static_cast<int64_t>(tm) * S::kTM + tile_row;
+      const int col = tn * S::kTN + half * S::kColsPerWarp;
+      constexpr bool kSum = kMode == kLinearWgrad || !kPair;   // the warp's columns pass through registers
+      if constexpr (kSum) {
+        float acc[S::kColsPerWarp];
+        for (int s = 0; ok && s < n_st; s += chunk, ++c) {
+          if (!(ok = warp_wait(wd, &bars.acc_full[c & 1], (c >> 1) & 1))) break;
+          tc_fence_after_sync();
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            if (n0 + c0 + j >= p.n) break;
-            float4 v = *reinterpret_cast<float4*>(o + j);
-            v.x += __uint_as_float(r[j]);
-            v.y += __uint_as_float(r[j + 1]);
-            v.z += __uint_as_float(r[j + 2]);
-            v.w += __uint_as_float(r[j + 3]);
-            *reinterpret_cast<float4*>(o + j) = v;
+          for (int c0 = 0; c0 < S::kColsPerWarp; c0 += 32) {
+            uint32_t r[32];
+            tmem_ld32(my_cols + static_cast<uint32_t>((c & 1) * S::kTN + c0), r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              acc[c0 + j] = s == 0 ? __uint_as_float(r[j]) : acc[c0 + j] + __uint_as_float(r[j]);
           }
-        } else {
-          switch (p.act) {
-            case kActRelu: finish32<kMode, kActRelu>(p, row, n0 + c0, r); break;
-            case kActSilu: finish32<kMode, kActSilu>(p, row, n0 + c0, r); break;
-            case kActGelu: finish32<kMode, kActGelu>(p, row, n0 + c0, r); break;
-            case kActGeluTanh: finish32<kMode, kActGeluTanh>(p, row, n0 + c0, r); break;
-            default: finish32<kMode, kActNone>(p, row, n0 + c0, r); break;
-          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(leader_empty[c & 1]);
         }
+        if (!ok) break;
+        if constexpr (kPair) {
+          if (row < p.m) {
+#pragma unroll
+            for (int c0 = 0; c0 < S::kColsPerWarp; c0 += 32)
+              finish32<kMode, kActNone>(p, row, col + c0, *reinterpret_cast<const float(*)[32]>(&acc[c0]));
+          }
+        } else if (row < p.m) {
+          // this CTA's part of the sum, into its own ring (idle: every stage
+          // it issued has been consumed)
+          float* part = reinterpret_cast<float*>(smem) + tile_row * kPartStride + half * S::kColsPerWarp;
+#pragma unroll
+          for (int j = 0; j < S::kColsPerWarp; j += 4)
+            *reinterpret_cast<float4*>(part + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+        }
+      } else {
+        if (!(ok = warp_wait(wd, &bars.acc_full[c & 1], (c >> 1) & 1))) break;
+        tc_fence_after_sync();
+        with_act<kMode>(p.act, [&](auto act) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < S::kColsPerWarp; c0 += 32) {
+            uint32_t r[32];
+            tmem_ld32(my_cols + static_cast<uint32_t>((c & 1) * S::kTN + c0), r);
+            tmem_ld_wait();
+            float f[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]);
+            if (row < p.m) finish32<kMode, decltype(act)::value>(p, row, col + c0, f);
+          }
+        });
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(leader_empty[c & 1]);
+        ++c;
       }
     }
   }
 
   tc_fence_before_sync();
   __syncthreads();
-  if (wd.aborted()) {
-    // a wait ran out: let the copies already in flight land first
-    if (warp == 0 && lane == 0) {
+  if (wd.aborted() && !skip) {
+    // a wait ran out: let the copies already in flight land first.  The odd
+    // CTA of a pair has them counted on the even one's barrier, whose phases
+    // it cannot rely on now: it gives them 100 us instead.
+    if (kPair && rank != 0) {
+      const long long t0 = clock64();
+      while (warp == 0 && lane == 0 && n_issued > 0 && clock64() - t0 < 200000) {
+      }
+    } else if (warp == 0 && lane == 0) {
       for (int st = 0; st < kStages && st < n_issued; ++st) {
         const int last = st + kStages * ((n_issued - 1 - st) / kStages);
         wd.drain(&bars.full[st], (last / kStages) & 1, 1000000);
@@ -278,20 +461,118 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
+  cluster_sync();          // nothing of this cluster touches another CTA's shared memory or TMEM from here,
+                           // but the split's reads of the partial tiles below
+  if constexpr (!kPair) {
+    // an aborted CTA's part is missing: every CTA then leaves its share out
+    bool whole = !skip;
+    for (int i = 0; i < ctas; ++i)
+      whole = whole && ld_cluster_u32(cluster_map(smem_u32(const_cast<int*>(&abort_flag)), i)) == 0u;
+    int tm, tn;
+    tiles.at(first_tile, &tm, &tn);
+    const int rows = min(128, p.m - tm * 128);
+    const int groups = min(128, p.n - tn * 128) / 8;           // of eight columns
+    if (whole) {
+      with_act<kMode>(p.act, [&](auto act) {
+        for (int u = static_cast<int>(rank) * kThreads + threadIdx.x; u < rows * groups; u += ctas * kThreads) {
+          const int r = u / groups, g = u - r * groups;
+          const uint32_t at = smem_u32(smem) + static_cast<uint32_t>((r * kPartStride + 8 * g) * 4);
+          float v[8] = {};
+          for (int i = 0; i < ctas; ++i) {
+            const uint32_t from = cluster_map(at, i);
+            const float4 x = ld_cluster_v4(from), y = ld_cluster_v4(from + 16);
+            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+            v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+          }
+          finish8<kMode, decltype(act)::value>(p, static_cast<int64_t>(tm) * 128 + r, tn * 128 + 8 * g, v);
+        }
+      });
+    }
+    cluster_sync();        // the parts have been read
+  }
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, kTmemCols);
+    if constexpr (kPair) tmem_dealloc_pair(tmem, S::kTmemCols);
+    else tmem_dealloc(tmem, S::kTmemCols);
   }
 }
 
-template <int kMode>
-cudaError_t launch_mode(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(linear_bf16_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSmemAlloc);
+template <int kMode, bool kPair>
+cudaError_t launch_shape(const LinearMaps& maps, const LinearParams& p, unsigned grid, unsigned cluster,
+                         cudaStream_t s) {
+  auto* kernel = linear_bf16_kernel<kMode, kPair>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
   if (e != cudaSuccess) return e;
-  const int64_t grid = static_cast<int64_t>((p.m + kTM - 1) / kTM) * ((p.n + kTN - 1) / kTN);
-  linear_bf16_kernel<kMode><<<static_cast<unsigned>(grid), kThreads, kSmemAlloc, s>>>(maps.a, maps.b, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemAlloc;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps.a, maps.b, p);
+}
+
+// Pairs that the device runs at once (one CTA per SM; an SM without a partner
+// in its group stays out), looked up once per device.
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_pairs[kMaxDevices];
+
+template <int kMode>
+cudaError_t resident_pairs(int* pairs, int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if ((e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  *pairs = g_pairs[dev].load(std::memory_order_relaxed);
+  if (*pairs > 0) return cudaSuccess;
+  auto* kernel = linear_bf16_kernel<kMode, true>;
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc)) != cudaSuccess)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * 256);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemAlloc;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaOccupancyMaxActiveClusters(pairs, kernel, &cfg)) != cudaSuccess) return e;
+  if (*pairs < 1) return cudaErrorLaunchOutOfResources;
+  g_pairs[dev].store(*pairs, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
+template <int kMode>
+cudaError_t launch_mode(const LinearMaps& maps, LinearParams p, cudaStream_t s) {
+  int pairs = 0, sms = 0;
+  cudaError_t e = resident_pairs<kMode>(&pairs, &sms);
+  if (e != cudaSuccess) return e;
+  const int64_t stages = (static_cast<int64_t>(p.k) + kTK - 1) / kTK;
+  const int64_t big = static_cast<int64_t>((p.m + 255) / 256) * ((p.n + 255) / 256);
+  const int64_t small = static_cast<int64_t>((p.m + 127) / 128) * ((p.n + 127) / 128);
+  // CTAs per small tile: as many as fit beside each other, up to a stage each
+  int64_t split = sms / small;
+  split = split < 1 ? 1 : split > kMaxSplit ? kMaxSplit : split;
+  if (split > stages) split = stages;
+  const int64_t pair_cost = ((big + pairs - 1) / pairs) * stages * kPairStageCost + kPairFixedCost;
+  const int64_t split_cost = ((small * split + sms - 1) / sms) * ((stages + split - 1) / split * kSplitStageCost + kSplitFixedCost);
+  if (pair_cost <= split_cost) {
+    const int64_t grid = 2 * (big < pairs ? big : pairs);
+    return launch_shape<kMode, true>(maps, p, static_cast<unsigned>(grid), 2, s);
+  }
+  p.split = static_cast<int>(split);
+  p.a_bytes = kOperandBytes;
+  return launch_shape<kMode, false>(maps, p, static_cast<unsigned>(small * split), static_cast<unsigned>(split), s);
 }
 
 // ---------------------------------------------------------------------------

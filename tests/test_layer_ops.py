@@ -153,6 +153,18 @@ def test_linear_wgrad(rows, k, n, bias):
     _within("dbias", db_d, dref, (rows / 128 + 10) * U_F32 * dmags if bias else torch.zeros_like(dref) + 1e-300)
 
 
+def test_linear_wgrad_keeps_float32_over_long_contractions():
+    """Over thousands of rows of one sign a running sum on the tensor core
+    alone would drift by a truncation per addition; the bound here is the one
+    of the module's head, 2^-18 at 16384 rows, and the drift would pass it."""
+    rows, k, n = 16384, 128, 256
+    x, g = _rand(13, rows, k).abs(), _rand(14, rows, n).abs()
+    dw = torch.zeros((k, n), device="cuda")
+    binding.linear_wgrad(x.cuda(), g.cuda(), dw)
+    ref = x.double().t() @ g.double()
+    _within("dw", dw, ref, ((32 + 16) * 2.0 ** -23 + (rows / 512 + 2) * U_F32) * ref)
+
+
 def test_linear_strided_operands_and_neighbours():
     """Rows of wider matrices: what lies between and behind the rows is NaN
     and must neither be read into the result nor written."""
