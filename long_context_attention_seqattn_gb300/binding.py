@@ -170,7 +170,7 @@ def load_library(path=LIB_PATH):
 
 
 def _check(status):
-    if status != SEQATTN_OK:
+    if status:
         lib = load_library()
         raise SeqattnError(status, lib.seqattn_last_error().decode())
 
@@ -306,62 +306,89 @@ def _act_code(act):
     return ACTIVATIONS[act]
 
 
-def _here(t, name, dtype):
-    """``t`` is a CUDA tensor of ``dtype`` on the current device."""
+# These calls are short on the device, so the checks are written for the usual
+# case: one look at each tensor's type, device, shape and strides (about 0.5 us
+# a tensor), and the words of a refusal are put together only when it is due.
+
+_bf16 = torch.bfloat16
+_f32 = torch.float32
+
+
+def _refuse(t, name, dtype):
     if not t.is_cuda or t.dtype != dtype:
         raise ValueError(f"{name} must be a CUDA tensor of {dtype}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
-def _matrix(t, name, cols=None, rows=None, dtype=torch.bfloat16):
-    """(rows, columns, row stride) of a tensor seen as a matrix of its last
-    dimension; the leading dimensions must lie at one uniform row stride."""
-    _here(t, name, dtype)
+def _device(t, name, dtype):
+    """Index of the current device, for a call whose first tensor is ``t``."""
+    if t.get_device() < 0:
+        _refuse(t, name, dtype)
+    return torch._C._cuda_getDevice()
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _matrix(t, name, cols, rows, dev, dtype=_bf16):
+    """(rows, row stride) of a tensor seen as a matrix of its last dimension;
+    the leading dimensions must lie at one uniform row stride."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, dtype)
     shape, stride = t.shape, t.stride()
-    if len(shape) < 2:
+    if len(shape) == 2:
+        r, c = shape
+        ld = stride[0] if r > 1 else c
+    elif len(shape) < 2:
         raise ValueError(f"{name} must have at least two dimensions")
-    c = shape[-1]
-    if c > 1 and stride[-1] != 1:
+    else:
+        r, c, ld = 1, shape[-1], None
+        for size, st in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+            if size == 1:
+                continue
+            if ld is None:
+                ld = st
+            elif st != r * ld and size * r:
+                raise ValueError(f"the rows of {name} must lie at one uniform stride")
+            r *= size
+        if ld is None or r <= 1:
+            ld = c
+    if stride[-1] != 1 and c > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    r, ld = 1, None
-    for size, st in zip(reversed(shape[:-1]), reversed(stride[:-1])):
-        if size == 0:
-            r = 0
-            break
-        if size == 1:
-            continue
-        if ld is None:
-            ld = st
-        elif st != r * ld:
-            raise ValueError(f"the rows of {name} must lie at one uniform stride")
-        r *= size
-    if cols is not None and c != cols:
+    if c != cols:
         raise ValueError(f"{name} has {c} columns, expected {cols}")
     if rows is not None and r != rows:
         raise ValueError(f"{name} has {r} rows, expected {rows}")
-    return r, c, c if ld is None else ld
+    return r, ld
 
 
-def _weight(w):
-    _here(w, "w", torch.bfloat16)
+def _weight(w, dev):
+    if w.dtype is not _bf16 or w.get_device() != dev:
+        _refuse(w, "w", _bf16)
     if w.dim() != 2 or not w.is_contiguous():
         raise ValueError("w must be a contiguous [k, n] matrix")
     return w.shape
 
 
-def _vector(t, name, n, dtype):
-    _here(t, name, dtype)
-    if tuple(t.shape) != (n,) or not t.is_contiguous():
+def _vector(t, name, n, dtype, dev):
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, dtype)
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} elements")
+    return t.data_ptr()
+
+
+def _dense(t, name, shape, dtype, dev):
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, dtype)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
-
-
-def _raw_stream(stream):
-    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
 
 
 def linear_fwd(x, w, y, bias=None, act="none", residual=None, z=None, stream=None):
@@ -369,19 +396,19 @@ def linear_fwd(x, w, y, bias=None, act="none", residual=None, z=None, stream=Non
     ``y``, ``residual`` [..., n] bf16 with rows at a uniform stride, ``w``
     [k, n] and ``bias`` [n] bf16.  ``z`` [..., n] bf16, if given, receives the
     pre-activation x w + bias.  ``residual`` may be ``y``."""
-    k, n = _weight(w)
-    rows, _, ldx = _matrix(x, "x", k)
-    _, _, ldy = _matrix(y, "y", n, rows)
+    dev = _device(w, "w", _bf16)
+    k, n = _weight(w, dev)
+    rows, ldx = _matrix(x, "x", k, None, dev)
+    _, ldy = _matrix(y, "y", n, rows, dev)
     ldr = ldz = 0
-    if bias is not None:
-        _vector(bias, "bias", n, torch.bfloat16)
+    b = None if bias is None else _vector(bias, "bias", n, _bf16, dev)
     if residual is not None:
-        _, _, ldr = _matrix(residual, "residual", n, rows)
+        _, ldr = _matrix(residual, "residual", n, rows, dev)
     if z is not None:
-        _, _, ldz = _matrix(z, "z", n, rows)
-    _check(load_library().seqattn_linear_fwd(rows, k, n, x.data_ptr(), ldx, w.data_ptr(), _addr(bias),
-                                             _act_code(act), _addr(residual), ldr, _addr(z), ldz, y.data_ptr(), ldy,
-                                             _raw_stream(stream)))
+        _, ldz = _matrix(z, "z", n, rows, dev)
+    _check((_lib or load_library()).seqattn_linear_fwd(
+        rows, k, n, x.data_ptr(), ldx, w.data_ptr(), b, _act_code(act), _addr(residual), ldr, _addr(z), ldz,
+        y.data_ptr(), ldy, _raw_stream(stream, dev)))
 
 
 def linear_dgrad(g, w, dx, act="none", z=None, residual=None, stream=None):
@@ -391,20 +418,21 @@ def linear_dgrad(g, w, dx, act="none", z=None, residual=None, stream=None):
     ``linear_fwd`` of the layer before kept it).  ``g`` [..., n], ``dx``,
     ``z``, ``residual`` [..., k] bf16, ``w`` [k, n].  ``residual`` may be
     ``dx`` (several gradients of one input are summed that way)."""
-    k, n = _weight(w)
+    dev = _device(w, "w", _bf16)
+    k, n = _weight(w, dev)
     code = _act_code(act)
-    rows, _, ldg = _matrix(g, "g", n)
-    _, _, lddx = _matrix(dx, "dx", k, rows)
+    rows, ldg = _matrix(g, "g", n, None, dev)
+    _, lddx = _matrix(dx, "dx", k, rows, dev)
     ldr = ldz = 0
     if residual is not None:
-        _, _, ldr = _matrix(residual, "residual", k, rows)
+        _, ldr = _matrix(residual, "residual", k, rows, dev)
     if code:
         if z is None:
             raise ValueError("z is needed when act is given")
-        _, _, ldz = _matrix(z, "z", k, rows)
-    _check(load_library().seqattn_linear_dgrad(rows, k, n, g.data_ptr(), ldg, w.data_ptr(), code,
-                                               z.data_ptr() if code else None, ldz, _addr(residual), ldr,
-                                               dx.data_ptr(), lddx, _raw_stream(stream)))
+        _, ldz = _matrix(z, "z", k, rows, dev)
+    _check((_lib or load_library()).seqattn_linear_dgrad(
+        rows, k, n, g.data_ptr(), ldg, w.data_ptr(), code, z.data_ptr() if code else None, ldz, _addr(residual), ldr,
+        dx.data_ptr(), lddx, _raw_stream(stream, dev)))
 
 
 def linear_wgrad(x, g, dw, dbias=None, stream=None):
@@ -412,15 +440,14 @@ def linear_wgrad(x, g, dw, dbias=None, stream=None):
     [..., n] bf16 with rows at a uniform stride, ``dw`` [k, n] and ``dbias``
     [n] float32, accumulated.  (``proj_wgrad`` is the form for float32 g of
     whole [B, T, ...] gradients.)"""
-    rows, k, ldx = _matrix(x, "x")
-    _, n, ldg = _matrix(g, "g", None, rows)
-    _here(dw, "dw", torch.float32)
-    if tuple(dw.shape) != (k, n) or not dw.is_contiguous():
-        raise ValueError(f"dw must be a contiguous [{k}, {n}] matrix")
-    if dbias is not None:
-        _vector(dbias, "dbias", n, torch.float32)
-    _check(load_library().seqattn_linear_wgrad(rows, k, n, x.data_ptr(), ldx, g.data_ptr(), ldg, dw.data_ptr(),
-                                               _addr(dbias), _raw_stream(stream)))
+    dev = _device(x, "x", _bf16)
+    k, n = x.shape[-1], g.shape[-1]
+    rows, ldx = _matrix(x, "x", k, None, dev)
+    _, ldg = _matrix(g, "g", n, rows, dev)
+    w = _dense(dw, "dw", (k, n), _f32, dev)
+    b = None if dbias is None else _vector(dbias, "dbias", n, _f32, dev)
+    _check((_lib or load_library()).seqattn_linear_wgrad(rows, k, n, x.data_ptr(), ldx, g.data_ptr(), ldg, w, b,
+                                                         _raw_stream(stream, dev)))
 
 
 def rope_plan(inv_freq, axis=None, interleaved=False):
@@ -449,43 +476,29 @@ def rope_plan(inv_freq, axis=None, interleaved=False):
 _TWO_PI = Fraction(6283185307179586476925286766559005768394, 10 ** 39)
 
 
-def _head_rows(t, name, B, c, H, d, dtype):
+def _head_rows(t, name, shape, dtype, dev):
     """Row stride of a [B, c, H, d] tensor whose heads are dense and whose rows
     (b, r) lie at one uniform stride."""
-    _here(t, name, dtype)
-    if tuple(t.shape) != (B, c, H, d):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, c, H, d)}")
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    B, c, H, d = shape
     sb, sc, sh, sd = t.stride()
-    if sd != 1 or (H > 1 and sh != d):
+    if sd != 1 or (sh != d and H > 1):
         raise ValueError(f"the heads of {name} must be dense")
-    if c == 0:
-        return H * d
     if c > 1:
         if B > 1 and sb != c * sc:
             raise ValueError(f"the rows of {name} must lie at one uniform stride")
         return sc
-    return sb if B > 1 else H * d
+    return sb if B > 1 and c == 1 else H * d
 
 
-def _rope_args(q, k_like, gamma_q, gamma_k, plan, positions, dtype):
-    """Problem, shape and pointers that the forward and backward share."""
-    B, c, Hq, d = q.shape
-    Bk, T, Hkv, dk = k_like.shape
-    if Bk != B or dk != d:
-        raise ValueError(f"caches of shape {tuple(k_like.shape)} do not go with queries of shape {tuple(q.shape)}")
-    if (gamma_q is None) != (gamma_k is None):
-        raise ValueError("gamma_q and gamma_k must both be given or both be None")
-    if gamma_q is not None:
-        _vector(gamma_q, "gamma_q", d, dtype)
-        _vector(gamma_k, "gamma_k", d, dtype)
-    if positions is not None:
-        axes = plan.axes if plan is not None else 1
-        _here(positions, "positions", torch.int64)
-        if positions.dim() == 2 and axes == 1:
-            positions = positions[None]
-        if tuple(positions.shape) != (axes, B, c) or not positions.is_contiguous():
-            raise ValueError(f"positions must be a contiguous int64 tensor of shape {(axes, B, c)}")
-    return Problem(B, Hq, Hkv, d, T, _dtype_code(dtype)), B, c, Hq, Hkv, d, positions
+def _rope_positions(positions, plan, B, c, dev):
+    axes = plan.axes if plan is not None else 1
+    if positions.dim() == 2 and axes == 1:
+        positions = positions[None]
+    return _dense(positions, "positions", (axes, B, c), torch.int64, dev)
 
 
 def qk_norm_rope_fwd(q_in, k_in, v_in, q, k_cache, v_cache, q_start, gamma_q=None, gamma_k=None, eps=1e-6,
@@ -500,28 +513,38 @@ def qk_norm_rope_fwd(q_in, k_in, v_in, q, k_cache, v_cache, q_start, gamma_q=Non
     stride); ``v_in`` and ``v_cache`` may both be None.  ``positions``: int64
     [axes, B, c] (or [B, c]); by default row r is at position q_start + r."""
     dt = q.dtype
-    pb, B, c, Hq, Hkv, d, positions = _rope_args(q, k_cache, gamma_q, gamma_k, plan, positions, dt)
-    ldq = _head_rows(q_in, "q_in", B, c, Hq, d, dt)
-    ldk = _head_rows(k_in, "k_in", B, c, Hkv, d, dt)
+    dev = _device(q, "q", dt)
+    B, c, Hq, d = q.shape
+    cache = k_cache.shape
+    Hkv = cache[2]
+    if len(cache) != 4 or cache[0] != B or cache[3] != d:
+        raise ValueError(f"a cache of shape {tuple(cache)} does not go with queries of shape {tuple(q.shape)}")
     if (v_in is None) != (v_cache is None):
         raise ValueError("v_in and v_cache must both be given or both be None")
-    ldv = 0
-    _here(q, "q", dt)
-    _need(q, "q", dt)
-    _here(k_cache, "k_cache", dt)
-    _need(k_cache, "k_cache", dt)
+    if (gamma_q is None) != (gamma_k is None):
+        raise ValueError("gamma_q and gamma_k must both be given or both be None")
+    heads = (B, c, Hkv, d)
+    ldq = _head_rows(q_in, "q_in", (B, c, Hq, d), dt, dev)
+    ldk = _head_rows(k_in, "k_in", heads, dt, dev)
+    ldv, v_src, v_dst, gq, gk = 0, None, None, None, None
     if v_in is not None:
-        ldv = _head_rows(v_in, "v_in", B, c, Hkv, d, dt)
-        _here(v_cache, "v_cache", dt)
-        _need(v_cache, "v_cache", dt, k_cache.shape)
-    _check(load_library().seqattn_qk_norm_rope_fwd(
-        pb, q_start, c, q_in.data_ptr(), ldq, k_in.data_ptr(), ldk, _addr(v_in), ldv, _addr(gamma_q),
-        _addr(gamma_k), eps, plan, _addr(positions), q.data_ptr(), k_cache.data_ptr(), _addr(v_cache),
-        _raw_stream(stream)))
+        ldv, v_src = _head_rows(v_in, "v_in", heads, dt, dev), v_in.data_ptr()
+        v_dst = _dense(v_cache, "v_cache", cache, dt, dev)
+    if gamma_q is not None:
+        gq, gk = _vector(gamma_q, "gamma_q", d, dt, dev), _vector(gamma_k, "gamma_k", d, dt, dev)
+    _check((_lib or load_library()).seqattn_qk_norm_rope_fwd(
+        Problem(B, Hq, Hkv, d, cache[1], _dtype_code(dt)), q_start, c, q_in.data_ptr(), ldq, k_in.data_ptr(), ldk,
+        v_src, ldv, gq, gk, eps, plan,
+        None if positions is None else _rope_positions(positions, plan, B, c, dev),
+        _dense(q, "q", q.shape, dt, dev), _dense(k_cache, "k_cache", cache, dt, dev), v_dst,
+        _raw_stream(stream, dev)))
 
 
 def qk_norm_rope_bwd_workspace_size(head_dim):
     return int(load_library().seqattn_qk_norm_rope_bwd_workspace_size(Problem(1, 1, 1, head_dim, 1, SEQATTN_BF16)))
+
+
+_rope_ws_bytes = {}      # head_dim -> bytes
 
 
 def qk_norm_rope_bwd(q_in, k_in, dq, dk_accum, dv_accum, dq_in, dk_in, dv_in, q_start, gamma_q=None, gamma_k=None,
@@ -536,42 +559,46 @@ def qk_norm_rope_bwd(q_in, k_in, dq, dk_accum, dv_accum, dq_in, dk_in, dv_in, q_
     ``qk_norm_rope_bwd_workspace_size(d)`` bytes (allocated here when
     omitted).  ``dv_accum`` and ``dv_in`` may both be None."""
     dt = dq_in.dtype
-    pb, B, c, Hq, Hkv, d, positions = _rope_args(dq, dk_accum, gamma_q, gamma_k, plan, positions, dt)
-    _here(dq, "dq", torch.float32)
-    _need(dq, "dq", torch.float32)
-    _here(dk_accum, "dk_accum", torch.float32)
-    _need(dk_accum, "dk_accum", torch.float32)
-    lddq = _head_rows(dq_in, "dq_in", B, c, Hq, d, dt)
-    lddk = _head_rows(dk_in, "dk_in", B, c, Hkv, d, dt)
+    dev = _device(dq, "dq", _f32)
+    B, c, Hq, d = dq.shape
+    cache = dk_accum.shape
+    Hkv = cache[2]
+    if len(cache) != 4 or cache[0] != B or cache[3] != d:
+        raise ValueError(f"accumulators of shape {tuple(cache)} do not go with dq of shape {tuple(dq.shape)}")
     if (dv_accum is None) != (dv_in is None):
         raise ValueError("dv_accum and dv_in must both be given or both be None")
+    if (gamma_q is None) != (gamma_k is None):
+        raise ValueError("gamma_q and gamma_k must both be given or both be None")
+    queries, heads = (B, c, Hq, d), (B, c, Hkv, d)
+    lddq = _head_rows(dq_in, "dq_in", queries, dt, dev)
+    lddk = _head_rows(dk_in, "dk_in", heads, dt, dev)
     lddv = ldq = ldk = ws_bytes = 0
+    v_src = v_dst = xq = xk = gq = gk = dgq = dgk = ws = None
     if dv_in is not None:
-        lddv = _head_rows(dv_in, "dv_in", B, c, Hkv, d, dt)
-        _here(dv_accum, "dv_accum", torch.float32)
-        _need(dv_accum, "dv_accum", torch.float32, dk_accum.shape)
-    norm = gamma_q is not None
+        lddv, v_dst = _head_rows(dv_in, "dv_in", heads, dt, dev), dv_in.data_ptr()
+        v_src = _dense(dv_accum, "dv_accum", cache, _f32, dev)
     temp = False
-    if norm:
-        ldq = _head_rows(q_in, "q_in", B, c, Hq, d, dt)
-        ldk = _head_rows(k_in, "k_in", B, c, Hkv, d, dt)
+    if gamma_q is not None:
         if dgamma_q is None or dgamma_k is None:
             raise ValueError("dgamma_q and dgamma_k are needed with a norm")
-        _vector(dgamma_q, "dgamma_q", d, torch.float32)
-        _vector(dgamma_k, "dgamma_k", d, torch.float32)
+        ldq, xq = _head_rows(q_in, "q_in", queries, dt, dev), q_in.data_ptr()
+        ldk, xk = _head_rows(k_in, "k_in", heads, dt, dev), k_in.data_ptr()
+        gq, gk = _vector(gamma_q, "gamma_q", d, dt, dev), _vector(gamma_k, "gamma_k", d, dt, dev)
+        dgq = _vector(dgamma_q, "dgamma_q", d, _f32, dev)
+        dgk = _vector(dgamma_k, "dgamma_k", d, _f32, dev)
         temp = workspace is None
         if temp:
-            workspace = torch.empty(qk_norm_rope_bwd_workspace_size(d), dtype=torch.uint8, device=dq.device)
-        else:
-            _here(workspace, "workspace", torch.uint8)
-            if not workspace.is_contiguous():
-                raise ValueError("workspace must be contiguous")
+            if d not in _rope_ws_bytes:
+                _rope_ws_bytes[d] = qk_norm_rope_bwd_workspace_size(d)
+            workspace = torch.empty(_rope_ws_bytes[d], dtype=torch.uint8, device=dq.device)
         ws_bytes = workspace.numel()
-    _check(load_library().seqattn_qk_norm_rope_bwd(
-        pb, q_start, c, _addr(q_in) if norm else None, ldq, _addr(k_in) if norm else None, ldk, _addr(gamma_q),
-        _addr(gamma_k), eps, plan, _addr(positions), dq.data_ptr(), dk_accum.data_ptr(), _addr(dv_accum),
-        dq_in.data_ptr(), lddq, dk_in.data_ptr(), lddk, _addr(dv_in), lddv, _addr(dgamma_q) if norm else None,
-        _addr(dgamma_k) if norm else None, _addr(workspace) if norm else None, ws_bytes, _raw_stream(stream)))
+        ws = _dense(workspace, "workspace", workspace.shape, torch.uint8, dev)
+    _check((_lib or load_library()).seqattn_qk_norm_rope_bwd(
+        Problem(B, Hq, Hkv, d, cache[1], _dtype_code(dt)), q_start, c, xq, ldq, xk, ldk, gq, gk, eps, plan,
+        None if positions is None else _rope_positions(positions, plan, B, c, dev),
+        _dense(dq, "dq", dq.shape, _f32, dev), _dense(dk_accum, "dk_accum", cache, _f32, dev), v_src,
+        dq_in.data_ptr(), lddq, dk_in.data_ptr(), lddk, v_dst, lddv, dgq, dgk, ws, ws_bytes,
+        _raw_stream(stream, dev)))
     if temp and stream is not None:
         workspace.record_stream(stream)       # as in chunk_bwd
 
@@ -639,21 +666,25 @@ class AdamW:
         ``grad_scale`` may be one-element CUDA tensors (float32, int64,
         float32), read when the step runs: what a captured graph needs, since
         numbers are kept as they were at the capture."""
-        if self.device is not None and self.device.index != torch.cuda.current_device():
-            raise ValueError(f"the tensors are on {self.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-        a = AdamwParams(0.0, beta1, beta2, eps, 1.0, 0, None, None, None)
-        for name, value, dtype in (("lr", lr, torch.float32), ("grad_scale", grad_scale, torch.float32),
-                                   ("step", step, torch.int64)):
+        if not self.params:
+            return
+        dev = _device(self.params[0], "params[0]", _f32)
+        if self.params[0].get_device() != dev:
+            _refuse(self.params[0], "params[0]", _f32)
+        on_device = [None, None, None]
+        for i, (name, value, dtype) in enumerate((("lr", lr, _f32), ("grad_scale", grad_scale, _f32),
+                                                  ("step", step, torch.int64))):
             if isinstance(value, torch.Tensor):
-                _here(value, name, dtype)
+                if value.dtype is not dtype or value.get_device() != dev:
+                    _refuse(value, name, dtype)
                 if value.numel() != 1:
                     raise ValueError(f"{name} must have one element")
-                setattr(a, name + "_dev", value.data_ptr())
-            else:
-                setattr(a, name, value)
-        _check(load_library().seqattn_adamw_step(self._tensors, len(self.params), self.state_bits, a,
-                                                 _raw_stream(stream)))
+                on_device[i] = value.data_ptr()
+        lr_dev, scale_dev, step_dev = on_device
+        a = AdamwParams(0.0 if lr_dev else lr, beta1, beta2, eps, 1.0 if scale_dev else grad_scale,
+                        0 if step_dev else step, lr_dev, scale_dev, step_dev)
+        _check((_lib or load_library()).seqattn_adamw_step(self._tensors, len(self.params), self.state_bits, a,
+                                                           _raw_stream(stream, dev)))
 
 
 def sync_status(stream=None):
