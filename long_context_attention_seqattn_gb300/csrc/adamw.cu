@@ -5,8 +5,9 @@
 //   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 // p is the float32 master weight; a bf16 copy for the next forward is written
 // in the same pass.  Every operation is rounded to float32 by itself, in this
-// order (no contraction), so the result does not depend on how the compiler
-// fuses it; the 8-bit codes in particular are reproducible.
+// order (no contraction), so the states do not depend on how the compiler fuses
+// it: 8-bit codes in particular are reproducible.  Only the quotient of p's
+// step is the fast one (2 ulp of a term that is a small part of p).
 //
 // 8-bit states: 256 consecutive elements share one float32 scale, max |x| / 448,
 // and each is stored as the nearest e4m3 number of x / scale.  The second
@@ -65,7 +66,8 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-template <bool k8, int kCap>
+// kDev: scalars may come from the device.
+template <bool k8, bool kDev, int kCap>
 __global__ void __launch_bounds__(kThreads)
     adamw_kernel(const __grid_constant__ AdamwList<kCap> list, const __grid_constant__ AdamwHyper h) {
   // ---- tensor of this CTA (the last one that starts at or before it)
@@ -79,25 +81,23 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t block = static_cast<int64_t>(blockIdx.x - list.first[lo]) * kWarps + warp_id();   // 256-element block
   const int64_t e0 = block * kAdamwBlock;
 
-  // ---- the step's scalars (float64 where a power cancels)
-  __shared__ float sh_step_size, sh_inv_root;
-  if (threadIdx.x == 0) {
-    const float lr = h.lr_dev != nullptr ? *h.lr_dev : h.lr;
-    float step_size = h.step_size, inv_root = h.inv_root_bc2;
-    if (h.lr_dev != nullptr || h.step_dev != nullptr) {
+  // ---- the step's scalars
+  float lr = h.lr, step_size = h.step_size, inv_root = h.inv_root_bc2, gscale = h.grad_scale;
+  if constexpr (kDev) {
+    // one thread of the CTA raises the betas to the step (float64: 1 - beta^t cancels)
+    __shared__ float sh_step_size, sh_inv_root;
+    if (h.lr_dev != nullptr) lr = *h.lr_dev;
+    if (h.grad_scale_dev != nullptr) gscale = __fmul_rn(gscale, *h.grad_scale_dev);
+    if (threadIdx.x == 0) {
       const double n = static_cast<double>(h.step_dev != nullptr ? *h.step_dev : h.step);
-      step_size = static_cast<float>((h.lr_dev != nullptr ? static_cast<double>(lr) : h.lrd) / (1.0 - pow(h.beta1d, n)));
-      inv_root = __fdiv_rn(1.f, static_cast<float>(sqrt(1.0 - pow(h.beta2d, n))));
+      sh_step_size = static_cast<float>((h.lr_dev != nullptr ? static_cast<double>(lr) : h.lrd) / (1.0 - pow(h.beta1d, n)));
+      sh_inv_root = __fdiv_rn(1.f, static_cast<float>(sqrt(1.0 - pow(h.beta2d, n))));
     }
-    sh_step_size = step_size;
-    sh_inv_root = inv_root;
+    __syncthreads();
+    step_size = sh_step_size;
+    inv_root = sh_inv_root;
   }
-  __syncthreads();
   if (e0 >= t.n) return;                         // warp-uniform
-  const float step_size = sh_step_size, inv_root = sh_inv_root;
-  const float lr = h.lr_dev != nullptr ? *h.lr_dev : h.lr;
-  float gscale = h.grad_scale;
-  if (h.grad_scale_dev != nullptr) gscale = __fmul_rn(gscale, *h.grad_scale_dev);
   const float decay = __fsub_rn(1.f, __fmul_rn(lr, t.weight_decay));
 
   const int lane = lane_id();
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads)
       const float vn = __fadd_rn(__fmul_rn(h.beta2, vv), __fmul_rn(__fmul_rn(h.one_minus_beta2, gg), gg));
       const float root = __fsqrt_rn(vn);
       const float denom = __fadd_rn(__fmul_rn(root, inv_root), h.eps);
-      p[j][i] = __fsub_rn(__fmul_rn(p[j][i], decay), __fmul_rn(step_size, __fdiv_rn(mm, denom)));
+      p[j][i] = __fsub_rn(__fmul_rn(p[j][i], decay), __fmul_rn(step_size, __fdividef(mm, denom)));
       m[j][i] = mm;
       v[j][i] = k8 ? root : vn;
       if constexpr (k8) {
@@ -246,10 +246,14 @@ cudaError_t launch_list(const AdamwTensor* t, int count, int state_bits, const A
   }
   if (blocks == 0) return cudaSuccess;
   const unsigned grid = static_cast<unsigned>(blocks);
-  if (state_bits == 8)
-    adamw_kernel<true, kCap><<<grid, kThreads, 0, s>>>(list, h);
-  else
-    adamw_kernel<false, kCap><<<grid, kThreads, 0, s>>>(list, h);
+  const bool dev = h.lr_dev != nullptr || h.grad_scale_dev != nullptr || h.step_dev != nullptr;
+  if (state_bits == 8) {
+    if (dev) adamw_kernel<true, true, kCap><<<grid, kThreads, 0, s>>>(list, h);
+    else adamw_kernel<true, false, kCap><<<grid, kThreads, 0, s>>>(list, h);
+  } else {
+    if (dev) adamw_kernel<false, true, kCap><<<grid, kThreads, 0, s>>>(list, h);
+    else adamw_kernel<false, false, kCap><<<grid, kThreads, 0, s>>>(list, h);
+  }
   return cudaGetLastError();
 }
 
