@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 namespace seqattn {
 
 // Geometry of one chunk call, after validation.
@@ -74,13 +76,18 @@ cudaError_t launch_wgrad_bf16(const WgradMaps& maps, int32_t batch, int64_t row_
 // ---- linear layer: products with epilogues (tcgen05) ------------------------
 enum : int { kLinearFwd = 0, kLinearDgrad = 1, kLinearWgrad = 2 };
 enum : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
-// Contraction elements per pipeline stage; operand boxes are {64, 128 rows}
-// for an operand whose contraction index is contiguous, else {64, 64 rows},
-// 128-byte swizzle.
+// Contraction elements per pipeline stage.
 constexpr int kLinearStageK = 64;
 struct LinearMaps {
   CUtensorMap a, b;
+  CUtensorMap out;             // wgrad: float32 result, box {32, 32}, 128-byte swizzle
 };
+// Rows of an operand box of a K-major operand: a tile's 128.  A result of
+// fewer than 128 rows has its A in boxes of those rows, rounded up to the
+// swizzle's 8: the tile's other rows hold whatever the ring holds, and only
+// result rows that are never stored depend on them.
+constexpr int linear_a_rows(int64_t m) { return m >= 128 ? 128 : static_cast<int>((m + 7) / 8 * 8); }
+constexpr uint32_t linear_a_bytes(int64_t m) { return static_cast<uint32_t>(linear_a_rows(m) * kLinearStageK * 2); }
 struct LinearParams {
   int m, n, k;                 // result rows and columns, contraction length
   int act;
@@ -91,10 +98,14 @@ struct LinearParams {
   int64_t ldr, ldz, ldo;       // row strides in elements
   int split;                   // CTAs that share a tile (split shape)
   uint32_t a_bytes;            // bytes of one A tile's copies (split shape)
+  int a_blocked, b_blocked;    // MN-major operand's map has its 64-column blocks as a dimension
   unsigned int* err;
   long long wait_cycles;
 };
 cudaError_t launch_linear_bf16(int mode, const LinearMaps& maps, const LinearParams& p, cudaStream_t s);
+// forward of at most kLinearGemvRows rows without the tensor cores
+constexpr int kLinearGemvRows = 2;
+cudaError_t launch_linear_gemv(const LinearParams& p, const void* x, int64_t ldx, const void* w, cudaStream_t s);
 // dbias[j] += sum over rows of g[r, j] (bf16), in a fixed order
 cudaError_t launch_colsum_bf16(const void* g, int64_t ldg, int rows, int n, float* dbias, cudaStream_t s);
 
@@ -145,5 +156,26 @@ struct AdamwHyper {
 };
 constexpr int kAdamwBlock = 256;   // elements per 8-bit scale
 cudaError_t launch_adamw(const AdamwTensor* t, int count, int state_bits, const AdamwHyper& h, cudaStream_t s);
+
+// ---- launches that may overlap their predecessor's end (kernels with grid_wait) ---
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, unsigned cluster,
+                              cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
 
 }  // namespace seqattn

@@ -56,13 +56,15 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMnBlockBytes = kTK * 128;       // one 64-column block of an MN-major tile
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
-constexpr int kSmemAlloc = kStages * kStageBytes + 1024;
+constexpr int kBoxBytes = 32 * 128;            // a warp's staging box: 32 rows x 32 float32
+constexpr int kOffBox = kStages * kStageBytes;
+constexpr int kSmemAlloc = kOffBox + kEpiWarps * kBoxBytes + 1024;
 constexpr int kChunkStages = 8;                // wgrad: stages summed on the tensor core
 constexpr int kMaxSplit = 8;                   // CTAs of a split cluster (portable limit)
 constexpr int kPartStride = 128 + 4;           // floats between rows of a split CTA's partial tile
 // Cost model of the two shapes, in SM cycles (see launch_mode).
-constexpr int64_t kPairStageCost = 600, kPairFixedCost = 6000;
-constexpr int64_t kSplitStageCost = 500, kSplitFixedCost = 6000;
+constexpr int64_t kPairStageCost = 670, kPairFixedCost = 8000;
+constexpr int64_t kSplitStageCost = 260, kSplitBytesPerCycle = 64, kSplitFixedCost = 6000, kSplitJoinCost = 1500;
 static_assert(128 * kPartStride * 4 <= kStages * kStageBytes, "the partial tile is kept in the ring");
 
 template <bool kPair>
@@ -202,24 +204,22 @@ __host__ __device__ constexpr uint32_t kstep_off(int ks) {
   return static_cast<uint32_t>((kMn ? ks * 2048 : ks * 32) >> 4);
 }
 
-// One operand tile: 128 of its M/N index at `mn`, 64 of the contraction at `k`.
+// One operand tile (16 KB): 128 of its M/N index from `mn` on, 64 of the
+// contraction from `k` on.  One copy where the tensor map allows: the issuing
+// thread's time goes by the copy (halves issued by four lanes side by side
+// were slower, 280 against 247 us for 8192 x 4096 x 6144).  An MN-major tile is
+// two 64-column blocks; when the row length is a multiple of 64 the map has
+// the block as a dimension of its own and one box takes both.
 template <bool kMn, bool kPair>
-__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, uint32_t pair_bar,
-                                          int mn, int k) {
-  if constexpr (kPair) {
-    if constexpr (kMn) {
-      tma_load_2d_pair(dst, map, pair_bar, mn, k);
-      tma_load_2d_pair(dst + kMnBlockBytes, map, pair_bar, mn + 64, k);
-    } else {
-      tma_load_2d_pair(dst, map, pair_bar, k, mn);
-    }
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, bool blocked, uint32_t bar, int mn,
+                                          int k) {
+  if (kMn && blocked) {
+    tma_load_3d_at<kPair>(dst, map, bar, 0, k, mn >> 6);
+  } else if (kMn) {
+    tma_load_2d_at<kPair>(dst, map, bar, mn, k);
+    tma_load_2d_at<kPair>(dst + kMnBlockBytes, map, bar, mn + 64, k);
   } else {
-    if constexpr (kMn) {
-      tma_load_2d(dst, map, bar, mn, k);
-      tma_load_2d(dst + kMnBlockBytes, map, bar, mn + 64, k);
-    } else {
-      tma_load_2d(dst, map, bar, k, mn);
-    }
+    tma_load_2d_at<kPair>(dst, map, bar, k, mn);
   }
 }
 
@@ -239,7 +239,7 @@ struct Tiles {
 template <int kMode, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_bf16_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                       const __grid_constant__ LinearParams p) {
+                       const __grid_constant__ CUtensorMap map_out, const __grid_constant__ LinearParams p) {
   using S = Shape<kPair>;
   constexpr bool kAMn = kMode == kLinearWgrad;
   constexpr bool kBMn = kMode != kLinearDgrad;
@@ -257,7 +257,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = lane_id();
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    skip_sh = error_already_set(p.err) ? 1u : 0u;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars.full[i], 1);
       mbar_init(&bars.empty[i], 1);
@@ -272,7 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&map_a);
     prefetch_tensormap(&map_b);
+    if (kMode == kLinearWgrad && kPair) prefetch_tensormap(&map_out);
   }
+  grid_launch_dependents();
   if (warp == 1) {
     if constexpr (kPair) {
       tmem_alloc_pair(&tmem_base_sh, S::kTmemCols);
@@ -281,6 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_relinquish();
     }
   }
+  grid_wait();             // operands, outputs and the error word belong to earlier kernels until here
+  if (threadIdx.x == 0) skip_sh = error_already_set(p.err) ? 1u : 0u;
   __syncthreads();
   cluster_sync();          // barriers of every CTA of the cluster are ready
   tc_fence_after_sync();
@@ -317,17 +320,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int st = it % kStages;
           if (!(ok = wd.wait_sleep(&bars.empty[st], ((it / kStages) & 1) ^ 1))) break;
           uint8_t* stage = smem + st * kStageBytes;
-          uint32_t pair_bar = 0;
-          if constexpr (kPair) {
-            // both CTAs' copies count on the even CTA's barrier, which its
-            // producer arms with the bytes of both
-            pair_bar = cluster_map(smem_u32(&bars.full[st]), 0);
-            if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], 2 * kStageBytes);
-          } else {
-            mbar_arrive_expect_tx(&bars.full[st], p.a_bytes + kOperandBytes);
-          }
-          load_tile<kAMn, kPair>(stage, &map_a, &bars.full[st], pair_bar, m0, s * kTK);
-          load_tile<kBMn, kPair>(stage + kOperandBytes, &map_b, &bars.full[st], pair_bar, n0, s * kTK);
+          // both CTAs' copies of a pair count on the even CTA's barrier, which
+          // its producer arms with the bytes of both
+          uint32_t bar = smem_u32(&bars.full[st]);
+          if constexpr (kPair) bar = cluster_map(bar, 0);
+          if (!kPair || rank == 0)
+            mbar_arrive_expect_tx(&bars.full[st], kPair ? 2 * kStageBytes : p.a_bytes + kOperandBytes);
+          load_tile<kAMn, kPair>(stage, &map_a, p.a_blocked, bar, m0, s * kTK);
+          load_tile<kBMn, kPair>(stage + kOperandBytes, &map_b, p.b_blocked, bar, n0, s * kTK);
           n_issued = it + 1;
         }
       }
@@ -407,10 +407,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         if constexpr (kPair) {
-          if (row < p.m) {
+          // dw += the tile, 32 x 32 at a time through this warp's box: TMA adds
+          // it in L2 (float32, one addition an element), clipped at dw's edges
+          uint8_t* box = smem + kOffBox + (warp - 2) * kBoxBytes;
+          const int row0 = static_cast<int>(row) - lane;
 #pragma unroll
-            for (int c0 = 0; c0 < S::kColsPerWarp; c0 += 32)
-              finish32<kMode, kActNone>(p, row, col + c0, *reinterpret_cast<const float(*)[32]>(&acc[c0]));
+          for (int c0 = 0; c0 < S::kColsPerWarp; c0 += 32) {
+            if (lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                  make_float4(acc[c0 + 4 * j], acc[c0 + 4 * j + 1], acc[c0 + 4 * j + 2], acc[c0 + 4 * j + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && row0 < p.m && col + c0 < p.n) {
+              tma_reduce_add_2d(&map_out, box, col + c0, row0);
+              bulk_commit_group();
+            }
           }
         } else if (row < p.m) {
           // this CTA's part of the sum, into its own ring (idle: every stage
@@ -441,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++c;
       }
     }
+    if (kMode == kLinearWgrad && kPair && lane == 0) bulk_wait_group<0>();   // every addition has been made
   }
 
   tc_fence_before_sync();
@@ -497,82 +512,241 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// What the device runs at once, looked up once per device: CTA pairs, and
+// clusters of each size (one CTA per SM; SMs of a group that a whole cluster
+// does not fill stay out, so 48 clusters of 3 do not fit on 152 SMs).
+constexpr int kMaxDevices = 64;
+struct Residency {
+  std::atomic<int> pairs{0};
+  std::atomic<int> clusters[kMaxSplit + 1] = {};
+};
+Residency g_resident[kMaxDevices];
+
 template <int kMode, bool kPair>
-cudaError_t launch_shape(const LinearMaps& maps, const LinearParams& p, unsigned grid, unsigned cluster,
-                         cudaStream_t s) {
+cudaError_t max_clusters(int cluster, int* count) {
   auto* kernel = linear_bf16_kernel<kMode, kPair>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster) * 256u);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemAlloc;
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, maps.a, maps.b, p);
+  return cudaOccupancyMaxActiveClusters(count, kernel, &cfg);
 }
 
-// Pairs that the device runs at once (one CTA per SM; an SM without a partner
-// in its group stays out), looked up once per device.
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_pairs[kMaxDevices];
-
 template <int kMode>
-cudaError_t resident_pairs(int* pairs, int* sms) {
+cudaError_t residency(Residency** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if ((e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  *pairs = g_pairs[dev].load(std::memory_order_relaxed);
-  if (*pairs > 0) return cudaSuccess;
-  auto* kernel = linear_bf16_kernel<kMode, true>;
-  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc)) != cudaSuccess)
-    return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * 256);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemAlloc;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if ((e = cudaOccupancyMaxActiveClusters(pairs, kernel, &cfg)) != cudaSuccess) return e;
-  if (*pairs < 1) return cudaErrorLaunchOutOfResources;
-  g_pairs[dev].store(*pairs, std::memory_order_relaxed);
+  Residency& r = g_resident[dev];
+  *out = &r;
+  if (r.pairs.load(std::memory_order_acquire) > 0) return cudaSuccess;
+  int n = 0;
+  for (int c = 1; c <= kMaxSplit; ++c) {
+    if ((e = max_clusters<kMode, false>(c, &n)) != cudaSuccess) return e;
+    r.clusters[c].store(n, std::memory_order_relaxed);
+  }
+  if ((e = max_clusters<kMode, true>(2, &n)) != cudaSuccess) return e;
+  if (n < 1 || r.clusters[1].load(std::memory_order_relaxed) < 1) return cudaErrorLaunchOutOfResources;
+  r.pairs.store(n, std::memory_order_release);
   return cudaSuccess;
 }
 
 template <int kMode>
 cudaError_t launch_mode(const LinearMaps& maps, LinearParams p, cudaStream_t s) {
-  int pairs = 0, sms = 0;
-  cudaError_t e = resident_pairs<kMode>(&pairs, &sms);
+  cudaError_t e = cudaFuncSetAttribute(linear_bf16_kernel<kMode, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSmemAlloc);
   if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(linear_bf16_kernel<kMode, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+  if (e != cudaSuccess) return e;
+  Residency* res = nullptr;
+  if ((e = residency<kMode>(&res)) != cudaSuccess) return e;
+  const int pairs = res->pairs.load(std::memory_order_relaxed);
   const int64_t stages = (static_cast<int64_t>(p.k) + kTK - 1) / kTK;
   const int64_t big = static_cast<int64_t>((p.m + 255) / 256) * ((p.n + 255) / 256);
   const int64_t small = static_cast<int64_t>((p.m + 127) / 128) * ((p.n + 127) / 128);
-  // CTAs per small tile: as many as fit beside each other, up to a stage each
-  int64_t split = sms / small;
-  split = split < 1 ? 1 : split > kMaxSplit ? kMaxSplit : split;
-  if (split > stages) split = stages;
+  p.a_bytes = kMode == kLinearWgrad ? kOperandBytes : linear_a_bytes(p.m);
+  // Time of either shape: waves of tiles, each its stages and a fixed part.
   const int64_t pair_cost = ((big + pairs - 1) / pairs) * stages * kPairStageCost + kPairFixedCost;
-  const int64_t split_cost = ((small * split + sms - 1) / sms) * ((stages + split - 1) / split * kSplitStageCost + kSplitFixedCost);
-  if (pair_cost <= split_cost) {
-    const int64_t grid = 2 * (big < pairs ? big : pairs);
-    return launch_shape<kMode, true>(maps, p, static_cast<unsigned>(grid), 2, s);
+  const int64_t stage_cost = kSplitStageCost + static_cast<int64_t>(p.a_bytes) / kSplitBytesPerCycle;
+  int64_t split_cost = INT64_MAX;
+  for (int c = 1; c <= kMaxSplit && c <= stages; ++c) {
+    const int fit = res->clusters[c].load(std::memory_order_relaxed);
+    if (fit < 1) continue;
+    const int64_t cost = ((small + fit - 1) / fit) * ((stages + c - 1) / c * stage_cost + kSplitFixedCost) +
+                         (c > 1 ? kSplitJoinCost : 0);
+    if (cost < split_cost) {
+      split_cost = cost;
+      p.split = c;
+    }
   }
-  p.split = static_cast<int>(split);
-  p.a_bytes = kOperandBytes;
-  return launch_shape<kMode, false>(maps, p, static_cast<unsigned>(small * split), static_cast<unsigned>(split), s);
+  // (a pair copies whole tiles of A, so a result of fewer rows is left to the split shape)
+  if (pair_cost <= split_cost && p.a_bytes == kOperandBytes) {
+    const int64_t ctas = 2 * (big < pairs ? big : pairs);
+    return launch_overlapped(linear_bf16_kernel<kMode, true>, static_cast<unsigned>(ctas), kThreads, kSmemAlloc, 2, s,
+                             maps.a, maps.b, maps.out, p);
+  }
+  return launch_overlapped(linear_bf16_kernel<kMode, false>, static_cast<unsigned>(small * p.split), kThreads,
+                           kSmemAlloc, static_cast<unsigned>(p.split), s, maps.a, maps.b, maps.out, p);
+}
+
+// ---------------------------------------------------------------------------
+// forward of a few rows (a token, or one of each of a few sequences)
+//
+// Bound by reading W once.  Tensor-core tiles would multiply mostly zeros, and
+// their pipeline's start costs more than these products: here a warp reads 16
+// bytes a lane, 512 bytes of W in rows of kCols columns, straight into float32
+// FMAs for all R rows of x.  A block of 8 warps and a cluster of up to 8
+// blocks split the contraction of one strip of kCols columns; partial sums
+// meet in shared and distributed shared memory and are added in a fixed order.
+// ---------------------------------------------------------------------------
+constexpr int kGvThreads = 256;
+constexpr int kGvSlab = 1024;       // rows of W per x slab in shared memory
+constexpr int kGvLoads = 8;         // loads in flight per lane
+
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+template <int R, int kCols>
+__global__ void __launch_bounds__(kGvThreads)
+    linear_gemv_kernel(const __grid_constant__ LinearParams p, const __nv_bfloat16* __restrict__ x, int64_t ldx,
+                       const __nv_bfloat16* __restrict__ w) {
+  __shared__ __align__(16) float xs[kGvSlab][R];
+  __shared__ __align__(16) float part[kGvThreads / 32][R][kCols];
+  constexpr int kLanes = kCols / 8, kRows = 32 / kLanes;    // lanes across a strip, rows of W a warp reads at once
+  const int lane = lane_id(), warp = warp_id();
+  const int cs = p.split, rank = static_cast<int>(cluster_rank());
+  const int strip = blockIdx.x / cs;
+  const int col = strip * kCols + 8 * (lane % kLanes);
+  const bool in = col < p.n;
+  const int sub = lane / kLanes;          // which of the warp's rows of W
+  // this block's contraction rows
+  const int k0 = static_cast<int>(static_cast<int64_t>(p.k) * rank / cs);
+  const int k1 = static_cast<int>(static_cast<int64_t>(p.k) * (rank + 1) / cs);
+  uint64_t acc[R][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[r][i] = 0ull;
+  grid_launch_dependents();
+  grid_wait();
+  for (int s0 = k0; s0 < k1; s0 += kGvSlab) {
+    const int len = min(kGvSlab, k1 - s0);
+    // the slab's W rows of this lane: every kStep-th
+    uint4 q[kGvLoads];
+    const __nv_bfloat16* wp = w + static_cast<int64_t>(s0 + kRows * warp + sub) * p.n + col;
+    constexpr int kStep = kRows * (kGvThreads / 32);
+    int k = kRows * warp + sub;
+#pragma unroll
+    for (int j = 0; j < kGvLoads; ++j)
+      q[j] = in && k + j * kStep < len ? ld_stream(wp + static_cast<int64_t>(j) * kStep * p.n) : make_uint4(0, 0, 0, 0);
+    __syncthreads();                       // the previous slab of x has been used
+    for (int i = threadIdx.x; i < len * R; i += kGvThreads) {
+      const int r = i / len, kk = i - r * len;
+      xs[kk][r] = r < p.m ? __bfloat162float(x[r * ldx + s0 + kk]) : 0.f;
+    }
+    __syncthreads();
+    while (k < len) {
+      const __nv_bfloat16* next = wp + static_cast<int64_t>(kGvLoads) * kStep * p.n;
+#pragma unroll
+      for (int j = 0; j < kGvLoads; ++j) {
+        const int kk = k + j * kStep;
+        const uint4 v = q[j];
+        // the load that takes this one's place, one round ahead
+        q[j] = in && kk + kGvLoads * kStep < len ? ld_stream(next + static_cast<int64_t>(j) * kStep * p.n)
+                                                 : make_uint4(0, 0, 0, 0);
+        if (kk < len) {
+          const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+          uint64_t f[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            f[i] = f2_pack(__uint_as_float(word[i] << 16), __uint_as_float(word[i] & 0xffff0000u));
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float xv = xs[kk][r];
+            const uint64_t x2 = f2_pack(xv, xv);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][i] = f2_fma(f[i], x2, acc[r][i]);
+          }
+        }
+      }
+      k += kGvLoads * kStep;
+      wp = next;
+    }
+  }
+  // ---- sums of the warp's rows, of the block's warps, of the cluster
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_unpack(acc[r][i], v[2 * i], v[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int o = kLanes; o < 32; o <<= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if (sub == 0) {
+      float4* o = reinterpret_cast<float4*>(&part[warp][r][8 * lane]);
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < R * kCols; i += kGvThreads) {
+    float t = 0.f;
+#pragma unroll
+    for (int g = 0; g < kGvThreads / 32; ++g) t += part[g][i / kCols][i % kCols];
+    part[0][i / kCols][i % kCols] = t;
+  }
+  cluster_sync();
+  // 8-column groups of the R rows, dealt over the cluster's blocks
+  with_act<kLinearFwd>(p.act, [&](auto act) {
+    for (int u = rank * kGvThreads + threadIdx.x; u < R * (kCols / 8); u += cs * kGvThreads) {
+      const int r = u / (kCols / 8), c = strip * kCols + 8 * (u % (kCols / 8));
+      if (r >= p.m || c >= p.n) continue;
+      const uint32_t at = smem_u32(&part[0][r][c - strip * kCols]);
+      float v[8] = {};
+      for (int i = 0; i < cs; ++i) {
+        const uint32_t from = cluster_map(at, i);
+        const float4 a = ld_cluster_v4(from), b = ld_cluster_v4(from + 16);
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+      }
+      finish8<kLinearFwd, decltype(act)::value>(p, r, c, v);
+    }
+  });
+  cluster_sync();                          // the other blocks have read this one's part
+}
+
+template <int R, int kCols>
+cudaError_t gemv_strips(LinearParams p, const void* x, int64_t ldx, const void* w, cudaStream_t s) {
+  const int strips = (p.n + kCols - 1) / kCols;
+  // blocks enough for about two per SM, each with at least 64 rows of W
+  int split = (304 + strips - 1) / strips;
+  split = split > 8 ? 8 : split;
+  while (split > 1 && p.k / split < 64) --split;
+  p.split = split;
+  return launch_overlapped(linear_gemv_kernel<R, kCols>, static_cast<unsigned>(strips * split), kGvThreads, 0,
+                           static_cast<unsigned>(split), s, p, static_cast<const __nv_bfloat16*>(x), ldx,
+                           static_cast<const __nv_bfloat16*>(w));
+}
+
+// Wide strips read 256 consecutive bytes of W a row; a result of few columns
+// takes narrow ones (64 bytes), so that 8 blocks a strip still fill the SMs.
+template <int R>
+cudaError_t gemv_rows(const LinearParams& p, const void* x, int64_t ldx, const void* w, cudaStream_t s) {
+  return p.n >= 2048 ? gemv_strips<R, 128>(p, x, ldx, w, s) : gemv_strips<R, 32>(p, x, ldx, w, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -619,6 +793,10 @@ cudaError_t launch_linear_bf16(int mode, const LinearMaps& maps, const LinearPar
     case kLinearDgrad: return launch_mode<kLinearDgrad>(maps, p, s);
     default: return launch_mode<kLinearWgrad>(maps, p, s);
   }
+}
+
+cudaError_t launch_linear_gemv(const LinearParams& p, const void* x, int64_t ldx, const void* w, cudaStream_t s) {
+  return p.m <= 1 ? gemv_rows<1>(p, x, ldx, w, s) : gemv_rows<2>(p, x, ldx, w, s);
 }
 
 cudaError_t launch_colsum_bf16(const void* g, int64_t ldg, int rows, int n, float* dbias, cudaStream_t s) {

@@ -495,6 +495,37 @@ bool make_map_2d(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, i
   return r == CUDA_SUCCESS;
 }
 
+// The same matrix with its 64-column blocks as a third dimension (cols a
+// multiple of 64): box {64 columns, 64 rows, 2 blocks}.
+bool make_map_blocks(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  memset(m, 0, sizeof(*m));
+  cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, 128};
+  cuuint32_t box[3] = {64, kLinearStageK, 2};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// 2-D map over a dense float32 [rows, cols] matrix: box {32, 32}, 128-byte swizzle.
+bool make_map_f32(CUtensorMap* m, const void* base, int64_t rows, int64_t cols) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  memset(m, 0, sizeof(*m));
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 4};
+  cuuint32_t box[2] = {32, 32};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 seqattn_status check_ld(int64_t ld, int64_t cols, const char* name) {
   if (ld < cols || ld % 8 != 0 || ld > (int64_t{1} << 36))
     return fail(SEQATTN_ERR_INVALID_ARG, "row stride of %s (%lld) must be a multiple of 8 and at least %lld", name,
@@ -513,9 +544,9 @@ seqattn_status check_linear(int64_t rows, int32_t k, int32_t n, int32_t act) {
 }
 
 // Common end of the three linear calls: error word, wait limit, maps, launch.
-// Operand a carries the result's row index, b its column index; a tile of an
-// operand whose contiguous dimension is that index (MN-major) is a stage of
-// contraction rows high, of the other kind (K-major) 128 index rows.
+// Operand a carries the result's row index, b its column index.  An operand
+// whose contiguous dimension is that index (MN-major) is `mn` columns of
+// contraction rows, of the other kind (K-major) `mn` rows.
 seqattn_status run_linear(int mode, LinearParams& p, const void* a, int64_t lda, const void* b, int64_t ldb,
                           seqattn_stream_t stream) {
   unsigned int* err = nullptr;
@@ -523,12 +554,21 @@ seqattn_status run_linear(int mode, LinearParams& p, const void* a, int64_t lda,
   if (e != cudaSuccess) return cuda_fail(e, "error word");
   p.err = err;
   p.wait_cycles = g_wait_cycles.load(std::memory_order_relaxed);
-  const bool a_mn = mode == kLinearWgrad, b_mn = mode != kLinearDgrad;
+  if (mode == kLinearFwd && p.m <= kLinearGemvRows) {
+    e = launch_linear_gemv(p, a, lda, b, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "linear launch");
+  }
   LinearMaps maps;
-  const bool made = (a_mn ? make_map_2d(&maps.a, a, p.k, p.m, lda, kLinearStageK)
-                        : make_map_2d(&maps.a, a, p.m, p.k, lda, 128)) &&
-                  (b_mn ? make_map_2d(&maps.b, b, p.k, p.n, ldb, kLinearStageK)
-                        : make_map_2d(&maps.b, b, p.n, p.k, ldb, 128));
+  memset(&maps.out, 0, sizeof(maps.out));
+  auto mn_map = [&](CUtensorMap* m, const void* base, int64_t mn, int64_t ld, int* blocked) {
+    *blocked = mn % 64 == 0;
+    return *blocked ? make_map_blocks(m, base, p.k, mn, ld) : make_map_2d(m, base, p.k, mn, ld, kLinearStageK);
+  };
+  const bool made = (mode == kLinearWgrad ? mn_map(&maps.a, a, p.m, lda, &p.a_blocked)
+                                          : make_map_2d(&maps.a, a, p.m, p.k, lda, linear_a_rows(p.m))) &&
+                    (mode != kLinearDgrad ? mn_map(&maps.b, b, p.n, ldb, &p.b_blocked)
+                                          : make_map_2d(&maps.b, b, p.n, p.k, ldb, 128)) &&
+                    (mode != kLinearWgrad || make_map_f32(&maps.out, p.out, p.m, p.n));
   if (!made) return fail(SEQATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed for the operands of the product");
   e = launch_linear_bf16(mode, maps, p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ok() : cuda_fail(e, "linear launch");
