@@ -34,7 +34,7 @@
 // wgrad's result is float32, and a long running sum on the tensor core is not
 // quite: its additions truncate (measured: 9.1e-6 relative over 8192 rows,
 // against 9.5e-7 for a float32 library product).  So its products are summed
-// in TMEM for at most kChunkStages stages (512 rows); the epilogue warps add
+// in TMEM for at most kChunkStages stages (768 rows); the epilogue warps add
 // these partial sums in registers, rounding to nearest, while the next are
 // computed into the other buffer.  bf16 results need no such care.
 #include <cuda_bf16.h>
@@ -59,12 +59,14 @@ constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kBoxBytes = 32 * 128;            // a warp's staging box: 32 rows x 32 float32
 constexpr int kOffBox = kStages * kStageBytes;
 constexpr int kSmemAlloc = kOffBox + kEpiWarps * kBoxBytes + 1024;
-constexpr int kChunkStages = 8;                // wgrad: stages summed on the tensor core
+constexpr int kChunkStages = 12;               // wgrad: stages summed on the tensor core
 constexpr int kMaxSplit = 8;                   // CTAs of a split cluster (portable limit)
 constexpr int kPartStride = 128 + 4;           // floats between rows of a split CTA's partial tile
-// Cost model of the two shapes, in SM cycles (see launch_mode).
-constexpr int64_t kPairStageCost = 670, kPairFixedCost = 8000;
-constexpr int64_t kSplitStageCost = 260, kSplitBytesPerCycle = 64, kSplitFixedCost = 6000, kSplitJoinCost = 1500;
+// Cost model of the two shapes, in SM cycles (see launch_mode).  Measured: a
+// pair's stage 0.26 us alone and 0.31 with every SM busy; a split CTA's 0.24,
+// whatever A's rows (its four MMAs are issued in about 110 cycles each).
+constexpr int64_t kPairStageCost = 570, kPairFixedCost = 13000;
+constexpr int64_t kSplitStageCost = 455, kSplitFixedCost = 11500, kSplitJoinCost = 1500;
 static_assert(128 * kPartStride * 4 <= kStages * kStageBytes, "the partial tile is kept in the ring");
 
 template <bool kPair>
@@ -192,8 +194,19 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
   }
 }
 
+// v += the eight floats at shared address `at` of every CTA of the cluster, in
+// rank order.
+__device__ __forceinline__ void add_parts(uint32_t at, int ctas, float (&v)[8]) {
+  for (int i = 0; i < ctas; ++i) {
+    const uint32_t from = cluster_map(at, static_cast<uint32_t>(i));
+    const float4 x = ld_cluster_v4(from), y = ld_cluster_v4(from + 16);
+    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+    v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+  }
+}
+
 __device__ __forceinline__ bool warp_wait(Watchdog& wd, uint64_t* bar, uint32_t parity) {
-  const bool ok = wd.wait_sleep(bar, parity);
+  const bool ok = wd.wait(bar, parity);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -318,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n0 = tn * S::kTN + (kPair ? 128 * static_cast<int>(rank) : 0);
         for (int s = s_begin; s < s_end; ++s, ++it) {
           const int st = it % kStages;
-          if (!(ok = wd.wait_sleep(&bars.empty[st], ((it / kStages) & 1) ^ 1))) break;
+          if (!(ok = wd.wait(&bars.empty[st], ((it / kStages) & 1) ^ 1))) break;
           uint8_t* stage = smem + st * kStageBytes;
           // both CTAs' copies of a pair count on the even CTA's barrier, which
           // its producer arms with the bytes of both
@@ -341,13 +354,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int t = first_tile; ok && t < n_tiles; t += tile_step) {
         for (int s = 0; ok && s < n_st; ++c) {
-          if (!(ok = wd.wait_sleep(&bars.acc_empty[c & 1], ((c >> 1) & 1) ^ 1))) break;
+          if (!(ok = wd.wait(&bars.acc_empty[c & 1], ((c >> 1) & 1) ^ 1))) break;
           tc_fence_after_sync();
           const uint32_t d = tmem + static_cast<uint32_t>((c & 1) * S::kTN);
           const int s_chunk = min(n_st, s + chunk);
           for (bool first = true; s < s_chunk; ++s, ++it) {
             const int st = it % kStages;
-            if (!(ok = wd.wait_sleep(&bars.full[st], (it / kStages) & 1))) break;
+            if (!(ok = wd.wait(&bars.full[st], (it / kStages) & 1))) break;
             tc_fence_after_sync();
             const uint64_t off = static_cast<uint64_t>(st * (kStageBytes >> 4));
 #pragma unroll
@@ -493,12 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r = u / groups, g = u - r * groups;
           const uint32_t at = smem_u32(smem) + static_cast<uint32_t>((r * kPartStride + 8 * g) * 4);
           float v[8] = {};
-          for (int i = 0; i < ctas; ++i) {
-            const uint32_t from = cluster_map(at, i);
-            const float4 x = ld_cluster_v4(from), y = ld_cluster_v4(from + 16);
-            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-            v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
-          }
+          add_parts(at, ctas, v);
           finish8<kMode, decltype(act)::value>(p, static_cast<int64_t>(tm) * 128 + r, tn * 128 + 8 * g, v);
         }
       });
@@ -575,13 +583,12 @@ cudaError_t launch_mode(const LinearMaps& maps, LinearParams p, cudaStream_t s) 
   p.a_bytes = kMode == kLinearWgrad ? kOperandBytes : linear_a_bytes(p.m);
   // Time of either shape: waves of tiles, each its stages and a fixed part.
   const int64_t pair_cost = ((big + pairs - 1) / pairs) * stages * kPairStageCost + kPairFixedCost;
-  const int64_t stage_cost = kSplitStageCost + static_cast<int64_t>(p.a_bytes) / kSplitBytesPerCycle;
   int64_t split_cost = INT64_MAX;
   for (int c = 1; c <= kMaxSplit && c <= stages; ++c) {
     const int fit = res->clusters[c].load(std::memory_order_relaxed);
     if (fit < 1) continue;
-    const int64_t cost = ((small + fit - 1) / fit) * ((stages + c - 1) / c * stage_cost + kSplitFixedCost) +
-                         (c > 1 ? kSplitJoinCost : 0);
+    const int64_t cost = ((small + fit - 1) / fit) * ((stages + c - 1) / c * kSplitStageCost + kSplitFixedCost) +
+                         (c - 1) * kSplitJoinCost;
     if (cost < split_cost) {
       split_cost = cost;
       p.split = c;
@@ -717,12 +724,7 @@ __global__ void __launch_bounds__(kGvThreads)
       if (r >= p.m || c >= p.n) continue;
       const uint32_t at = smem_u32(&part[0][r][c - strip * kCols]);
       float v[8] = {};
-      for (int i = 0; i < cs; ++i) {
-        const uint32_t from = cluster_map(at, i);
-        const float4 a = ld_cluster_v4(from), b = ld_cluster_v4(from + 16);
-        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-      }
+      add_parts(at, cs, v);
       finish8<kLinearFwd, decltype(act)::value>(p, r, c, v);
     }
   });

@@ -8,9 +8,9 @@ linear    one bf16 rounding of the result, plus the float32 sums: the tensor
           additions (two more for bias and residual) of at most 2^-23 of the
           sum of magnitudes S; the activations' fast exponential adds
           2^-20 (1 + |z|) (its argument's rounding grows with |z|).
-weights   float32: products are summed for at most 512 rows on the tensor
-          core (32 additions of 2^-23) and those sums are added in float32
-          (one 2^-24 each, rows / 512 + 1 of them).
+weights   float32: products are summed for at most 768 rows on the tensor
+          core (48 additions of 2^-23) and those sums are added in float32
+          (one 2^-24 each, fewer than rows / 512 + 2 of them).
 rope      one rounding to the element type; in float32 about 24 roundings of
           a value no larger than the head's largest rotated pair.
 adamw     float32 states: at most 8 roundings of a term each.  8-bit states:
