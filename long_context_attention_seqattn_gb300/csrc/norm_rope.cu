@@ -274,6 +274,8 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocksPerSm)
   const Groups gr(p, HPW, p.v_in != nullptr);
   const LaneRotation<kInter> lr(p, l, lane, 1.f);
   int64_t at, end;
+  grid_launch_dependents();
+  grid_wait();
   stretch(static_cast<int64_t>(p.B) * p.q_len * gr.all, &at, &end);
   while (at < end) {
     const int64_t row = at / gr.all;
@@ -392,6 +394,8 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
   const LaneRotation<kInter> lr(p, l, lane, -1.f);
   uint64_t sq[4] = {}, sk[4] = {};               // float32 pairs of zeros
   int64_t at, end;
+  grid_launch_dependents();
+  grid_wait();
   stretch(static_cast<int64_t>(p.B) * p.q_len * gr.all, &at, &end);
   while (at < end) {
     const int64_t row = at / gr.all;
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(1024)
   const int e = blockIdx.x * 32 + lane;
   // launched while the backward still runs: wait until it has finished and its
   // partial sums are visible
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
   float t = 0.f;
 #pragma unroll 4
   for (int b = w; b < blocks; b += 32) t += partial[static_cast<int64_t>(b) * 2 * D + e];
@@ -493,11 +497,10 @@ template <typename E, int D>
 cudaError_t fwd_typed(const NormRopeParams& p, cudaStream_t s) {
   const unsigned grid = grid_for(p, 32 / (D / 8), p.v_in != nullptr, kSms * kFwdBlocksPerSm);
   const bool norm = p.gamma_q != nullptr, inter = p.interleaved != 0;
-  if (norm && inter) norm_rope_fwd_kernel<E, D, true, true><<<grid, kThreads, 0, s>>>(p);
-  else if (norm) norm_rope_fwd_kernel<E, D, true, false><<<grid, kThreads, 0, s>>>(p);
-  else if (inter) norm_rope_fwd_kernel<E, D, false, true><<<grid, kThreads, 0, s>>>(p);
-  else norm_rope_fwd_kernel<E, D, false, false><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  if (norm && inter) return launch_overlapped(norm_rope_fwd_kernel<E, D, true, true>, grid, kThreads, 0, 1, s, p);
+  if (norm) return launch_overlapped(norm_rope_fwd_kernel<E, D, true, false>, grid, kThreads, 0, 1, s, p);
+  if (inter) return launch_overlapped(norm_rope_fwd_kernel<E, D, false, true>, grid, kThreads, 0, 1, s, p);
+  return launch_overlapped(norm_rope_fwd_kernel<E, D, false, false>, grid, kThreads, 0, 1, s, p);
 }
 
 template <typename E, int D>
@@ -505,25 +508,15 @@ cudaError_t bwd_typed(const NormRopeParams& p, cudaStream_t s) {
   const unsigned grid = grid_for(p, 32 / (D / 8), p.dv_in != nullptr, kBwdBlocks);
   const bool inter = p.interleaved != 0;
   if (p.gamma_q == nullptr) {
-    if (inter) norm_rope_bwd_kernel<E, D, false, true><<<grid, kThreads, 0, s>>>(p);
-    else norm_rope_bwd_kernel<E, D, false, false><<<grid, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    if (inter) return launch_overlapped(norm_rope_bwd_kernel<E, D, false, true>, grid, kThreads, 0, 1, s, p);
+    return launch_overlapped(norm_rope_bwd_kernel<E, D, false, false>, grid, kThreads, 0, 1, s, p);
   }
-  if (inter) norm_rope_bwd_kernel<E, D, true, true><<<grid, kThreads, 0, s>>>(p);
-  else norm_rope_bwd_kernel<E, D, true, false><<<grid, kThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      inter ? launch_overlapped(norm_rope_bwd_kernel<E, D, true, true>, grid, kThreads, 0, 1, s, p)
+            : launch_overlapped(norm_rope_bwd_kernel<E, D, true, false>, grid, kThreads, 0, 1, s, p);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * D / 32);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_rope_dgamma_kernel<D>, static_cast<const float*>(p.partial),
-                            static_cast<int>(grid), p.dgamma_q, p.dgamma_k);
+  return launch_overlapped(norm_rope_dgamma_kernel<D>, 2 * D / 32, 1024, 0, 1, s,
+                           static_cast<const float*>(p.partial), static_cast<int>(grid), p.dgamma_q, p.dgamma_k);
 }
 
 }  // namespace
