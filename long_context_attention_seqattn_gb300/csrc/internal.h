@@ -96,12 +96,16 @@ struct LinearParams {
   __nv_bfloat16* z;            // pre-activation: written by the forward, read by dgrad
   void* out;                   // bf16 (forward, dgrad) or float32 accumulator (wgrad)
   int64_t ldr, ldz, ldo;       // row strides in elements
-  int split;                   // CTAs that share a tile (split shape)
+  // filled by plan_linear_bf16
+  int split;                   // CTAs that share a tile (split shape), 0: pair shape
+  int tile_n;                  // columns of a tile (pair shape)
+  int clusters;                // clusters launched
   uint32_t a_bytes;            // bytes of one A tile's copies (split shape)
   int a_blocked, b_blocked;    // MN-major operand's map has its 64-column blocks as a dimension
   unsigned int* err;
   long long wait_cycles;
 };
+cudaError_t plan_linear_bf16(int mode, LinearParams& p);
 cudaError_t launch_linear_bf16(int mode, const LinearMaps& maps, const LinearParams& p, cudaStream_t s);
 // forward of at most kLinearGemvRows rows without the tensor cores
 constexpr int kLinearGemvRows = 2;

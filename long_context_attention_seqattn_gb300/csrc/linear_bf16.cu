@@ -14,12 +14,13 @@
 // Rows, columns and contraction tails past the tensors arrive as TMA zeros.
 //
 // Two shapes of the kernel:
-//   pair   clusters of two CTAs, persistent.  A pair owns a 256 x 256 tile:
-//          one thread issues M256 N256 K16 MMAs for both SMs, each SM loads
-//          half of A (its 128 rows) and half of B (128 columns), 32 KB a stage
-//          of 64, and keeps its 128 x 256 half of the result in TMEM.  Two
-//          result buffers (512 columns): the epilogue of a tile runs under
-//          the products of the next.
+//   pair   clusters of two CTAs, persistent.  A pair owns a 256 x N tile (N =
+//          256, or a narrower one that fills the last wave better): one
+//          thread issues M256 K16 MMAs for both SMs, each SM loads half of A
+//          (its 128 rows) and half of B (N / 2 columns), at most 32 KB a
+//          stage of 64, and keeps its 128 x N half of the result in TMEM.
+//          Two result buffers (512 columns): the epilogue of a tile runs
+//          under the products of the next.
 //   split  clusters of 1 to 8 CTAs that share one 128 x 128 tile: CTA i sums
 //          the i-th part of the contraction, the parts meet in distributed
 //          shared memory and are added in order.  For results with few tiles
@@ -62,10 +63,12 @@ constexpr int kSmemAlloc = kOffBox + kEpiWarps * kBoxBytes + 1024;
 constexpr int kChunkStages = 12;               // wgrad: stages summed on the tensor core
 constexpr int kMaxSplit = 8;                   // CTAs of a split cluster (portable limit)
 constexpr int kPartStride = 128 + 4;           // floats between rows of a split CTA's partial tile
-// Cost model of the two shapes, in SM cycles (see launch_mode).  Measured: a
-// pair's stage 0.26 us alone and 0.31 with every SM busy; a split CTA's 0.24,
-// whatever A's rows (its four MMAs are issued in about 110 cycles each).
-constexpr int64_t kPairStageCost = 570, kPairFixedCost = 13000;
+// Cost model of the two shapes, in SM cycles (see plan_mode).  Measured with
+// every SM busy: a pair's stage 0.32 us with a tile of 256 columns and 0.27
+// with 128 (kPairStageCost, and kPairColumnCost for 128 columns more), so a
+// narrow tile pays only where it saves a wave; a split CTA's 0.24, whatever
+// A's rows (its four MMAs are issued in about 110 cycles each).
+constexpr int64_t kPairStageCost = 510, kPairColumnCost = 98, kPairFixedCost = 13000;
 constexpr int64_t kSplitStageCost = 455, kSplitFixedCost = 11500, kSplitJoinCost = 1500;
 static_assert(128 * kPartStride * 4 <= kStages * kStageBytes, "the partial tile is kept in the ring");
 
@@ -166,12 +169,12 @@ __device__ __forceinline__ void finish8(const LinearParams& p, int64_t row, int 
   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * p.ldo + col) = pack8(v);
 }
 
-// 32 consecutive columns of one row (as many as the result has).
+// 32 consecutive columns of one row, those below `end`.
 template <int kMode, int kAct>
-__device__ __forceinline__ void finish32(const LinearParams& p, int64_t row, int col, const float (&r)[32]) {
+__device__ __forceinline__ void finish32(const LinearParams& p, int64_t row, int col, int end, const float (&r)[32]) {
 #pragma unroll
   for (int j = 0; j < 32; j += 8) {
-    if (col + j >= p.n) break;
+    if (col + j >= end) break;
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = r[j + i];
@@ -305,7 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool skip = ld_cluster_u32(cluster_map(smem_u32(&skip_sh), 0)) != 0u;
 
   // ---- this cluster's tiles and this CTA's part of the contraction
-  const Tiles tiles = {(p.m + S::kTM - 1) / S::kTM, (p.n + S::kTN - 1) / S::kTN};
+  const int tile_n = kPair ? p.tile_n : S::kTN;
+  const Tiles tiles = {(p.m + S::kTM - 1) / S::kTM, (p.n + tile_n - 1) / tile_n};
   const int all_stages = (p.k + kTK - 1) / kTK;
   const int ctas = kPair ? 2 : p.split;
   const int first_tile = blockIdx.x / ctas;
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int tm, tn;
         tiles.at(t, &tm, &tn);
         const int m0 = tm * S::kTM + (kPair ? 128 * static_cast<int>(rank) : 0);
-        const int n0 = tn * S::kTN + (kPair ? 128 * static_cast<int>(rank) : 0);
+        const int n0 = tn * tile_n + (kPair ? tile_n / 2 * static_cast<int>(rank) : 0);
         for (int s = s_begin; s < s_end; ++s, ++it) {
           const int st = it % kStages;
           if (!(ok = wd.wait(&bars.empty[st], ((it / kStages) & 1) ^ 1))) break;
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && (!kPair || rank == 0)) {
-      const uint32_t idesc = make_idesc_bf16(S::kTM, S::kTN, kAMn, kBMn);
+      const uint32_t idesc = make_idesc_bf16(S::kTM, tile_n, kAMn, kBMn);
       const uint64_t a0 = make_desc_sw128(smem_u32(smem), kAMn ? kMnBlockBytes : 16, 1024);
       const uint64_t b0 = make_desc_sw128(smem_u32(smem) + kOperandBytes, kBMn ? kMnBlockBytes : 16, 1024);
       int it = 0, c = 0;       // stages and result buffers issued so far
@@ -388,7 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3;
     const int half = (warp - 2) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t my_cols = tmem + lane_base + static_cast<uint32_t>(half * S::kColsPerWarp);
+    const int warp_cols = tile_n / 2;
+    const uint32_t my_cols = tmem + lane_base + static_cast<uint32_t>(half * warp_cols);
     const int tile_row = (kPair ? 128 * static_cast<int>(rank) : 0) + quad * 32 + lane;
     const uint32_t leader_empty[2] = {cluster_map(smem_u32(&bars.acc_empty[0]), kPair ? 0 : rank),
                                       cluster_map(smem_u32(&bars.acc_empty[1]), kPair ? 0 : rank)};
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tm, tn;
       tiles.at(t, &tm, &tn);
       const int64_t row = static_cast<int64_t>(tm) * S::kTM + tile_row;
-      const int col = tn * S::kTN + half * S::kColsPerWarp;
+      const int col = tn * tile_n + half * warp_cols;
       constexpr bool kSum = kMode == kLinearWgrad || !kPair;   // the warp's columns pass through registers
       if constexpr (kSum) {
         float acc[S::kColsPerWarp];
@@ -452,14 +457,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         with_act<kMode>(p.act, [&](auto act) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < S::kColsPerWarp; c0 += 32) {
+          for (int c0 = 0; c0 < warp_cols; c0 += 32) {
             uint32_t r[32];
             tmem_ld32(my_cols + static_cast<uint32_t>((c & 1) * S::kTN + c0), r);
             tmem_ld_wait();
             float f[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]);
-            if (row < p.m) finish32<kMode, decltype(act)::value>(p, row, col + c0, f);
+            if (row < p.m) finish32<kMode, decltype(act)::value>(p, row, col + c0, min(p.n, col + warp_cols), f);
           }
         });
         tc_fence_before_sync();
@@ -567,8 +572,10 @@ cudaError_t residency(Residency** out) {
   return cudaSuccess;
 }
 
+// Chooses the shape for p.m x p.n with contraction p.k: the one, and the tile
+// width or split, whose waves of tiles take the least time in the cost model.
 template <int kMode>
-cudaError_t launch_mode(const LinearMaps& maps, LinearParams p, cudaStream_t s) {
+cudaError_t plan_mode(LinearParams& p) {
   cudaError_t e = cudaFuncSetAttribute(linear_bf16_kernel<kMode, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSmemAlloc);
   if (e != cudaSuccess) return e;
@@ -576,31 +583,49 @@ cudaError_t launch_mode(const LinearMaps& maps, LinearParams p, cudaStream_t s) 
   if (e != cudaSuccess) return e;
   Residency* res = nullptr;
   if ((e = residency<kMode>(&res)) != cudaSuccess) return e;
-  const int pairs = res->pairs.load(std::memory_order_relaxed);
   const int64_t stages = (static_cast<int64_t>(p.k) + kTK - 1) / kTK;
-  const int64_t big = static_cast<int64_t>((p.m + 255) / 256) * ((p.n + 255) / 256);
+  p.a_bytes = kMode == kLinearWgrad ? kOperandBytes : static_cast<uint32_t>(linear_a_rows(p.m) * kTK * 2);
+  int64_t best = INT64_MAX;
+  // a pair copies whole tiles of A, so a result of fewer rows is left to the split shape
+  if (p.a_bytes == kOperandBytes) {
+    const int pairs = res->pairs.load(std::memory_order_relaxed);
+    // widths: wgrad's epilogue adds 32-column boxes of a half; a forward whose
+    // W comes in whole blocks (see load_tile) would lose that with halves that
+    // are not (2048 x 4096 x 4096 with 240 columns: 62 us, 50 with 256)
+    const int step = kMode == kLinearDgrad || (kMode == kLinearFwd && p.n % 64 != 0) ? 16 : 128;
+    for (int tn = 256; tn >= (kMode == kLinearWgrad ? 256 : 128); tn -= step) {
+      const int64_t tiles = static_cast<int64_t>((p.m + 255) / 256) * ((p.n + tn - 1) / tn);
+      const int64_t cost =
+          ((tiles + pairs - 1) / pairs) * stages * (kPairStageCost + kPairColumnCost * (tn - 128) / 128) + kPairFixedCost;
+      if (cost < best) {
+        best = cost;
+        p.tile_n = tn;
+        p.clusters = static_cast<int>(tiles < pairs ? tiles : pairs);
+        p.split = 0;
+      }
+    }
+  }
   const int64_t small = static_cast<int64_t>((p.m + 127) / 128) * ((p.n + 127) / 128);
-  p.a_bytes = kMode == kLinearWgrad ? kOperandBytes : linear_a_bytes(p.m);
-  // Time of either shape: waves of tiles, each its stages and a fixed part.
-  const int64_t pair_cost = ((big + pairs - 1) / pairs) * stages * kPairStageCost + kPairFixedCost;
-  int64_t split_cost = INT64_MAX;
   for (int c = 1; c <= kMaxSplit && c <= stages; ++c) {
     const int fit = res->clusters[c].load(std::memory_order_relaxed);
-    if (fit < 1) continue;
+    if (fit < 1 || small > INT32_MAX / kMaxSplit) continue;
     const int64_t cost = ((small + fit - 1) / fit) * ((stages + c - 1) / c * kSplitStageCost + kSplitFixedCost) +
                          (c - 1) * kSplitJoinCost;
-    if (cost < split_cost) {
-      split_cost = cost;
+    if (cost < best) {
+      best = cost;
+      p.clusters = static_cast<int>(small);
       p.split = c;
     }
   }
-  // (a pair copies whole tiles of A, so a result of fewer rows is left to the split shape)
-  if (pair_cost <= split_cost && p.a_bytes == kOperandBytes) {
-    const int64_t ctas = 2 * (big < pairs ? big : pairs);
-    return launch_overlapped(linear_bf16_kernel<kMode, true>, static_cast<unsigned>(ctas), kThreads, kSmemAlloc, 2, s,
-                             maps.a, maps.b, maps.out, p);
-  }
-  return launch_overlapped(linear_bf16_kernel<kMode, false>, static_cast<unsigned>(small * p.split), kThreads,
+  return cudaSuccess;
+}
+
+template <int kMode>
+cudaError_t launch_mode(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
+  if (p.split == 0)
+    return launch_overlapped(linear_bf16_kernel<kMode, true>, 2u * static_cast<unsigned>(p.clusters), kThreads,
+                             kSmemAlloc, 2, s, maps.a, maps.b, maps.out, p);
+  return launch_overlapped(linear_bf16_kernel<kMode, false>, static_cast<unsigned>(p.clusters) * p.split, kThreads,
                            kSmemAlloc, static_cast<unsigned>(p.split), s, maps.a, maps.b, maps.out, p);
 }
 
@@ -752,42 +777,97 @@ cudaError_t gemv_rows(const LinearParams& p, const void* x, int64_t ldx, const v
 }
 
 // ---------------------------------------------------------------------------
-// column sums of a bf16 matrix, dbias[j] += sum_r g[r, j], in a fixed order:
-// one block owns 32 columns and every row; thread (y, x) sums rows y, y + 64,
-// ... of eight columns, then the block adds its 64 partial rows in a tree.
+// column sums of a bf16 matrix, dbias[j] += sum_r g[r, j], in a fixed order
+//
+// Bound by reading g once.  A warp reads two rows of a strip of 128 columns, 16
+// bytes a lane; a block of 8 warps, and a cluster of up to 8 blocks when there
+// are rows for them, share the strip's rows.  A lane keeps four sums per column;
+// they, the warps and the blocks are added as trees.  Three blocks an SM, so
+// that the clusters all run at once: with 100 registers a thread 46 clusters
+// of 6 fit where 8192 x 6144 needs 48, and the call took 55 us.
 // ---------------------------------------------------------------------------
-constexpr int kSumCols = 32;
-constexpr int kSumRows = 128;
+constexpr int kSumThreads = 256;
+constexpr int kSumCols = 128;
+constexpr int kSumLoads = 8;        // loads in flight per lane
+constexpr int kSumAccs = 4;         // sums per lane and column
+constexpr int kSumSplit = 8;
 
-__global__ void __launch_bounds__(kSumRows * kSumCols / 8)
-    colsum_bf16_kernel(const __nv_bfloat16* __restrict__ g, int64_t ldg, int rows, int n, float* __restrict__ dbias) {
-  __shared__ float part[kSumRows][kSumCols + 1];
-  const int x = threadIdx.x % (kSumCols / 8), y = threadIdx.x / (kSumCols / 8);
-  const int col = blockIdx.x * kSumCols + 8 * x;
-  float acc[8] = {};
+__global__ void __launch_bounds__(kSumThreads, 3)
+    colsum_bf16_kernel(const __nv_bfloat16* __restrict__ g, int64_t ldg, int rows, int n, int split,
+                       float* __restrict__ dbias) {
+  __shared__ __align__(16) float part[kSumThreads / 32][kSumCols];
+  const int lane = lane_id(), warp = warp_id(), sub = lane >> 4;
+  const int rank = static_cast<int>(cluster_rank());
+  const int strip = blockIdx.x / split;
+  const int col = strip * kSumCols + 8 * (lane & 15);
+  const int r0 = static_cast<int>(static_cast<int64_t>(rows) * rank / split);
+  const int r1 = static_cast<int>(static_cast<int64_t>(rows) * (rank + 1) / split);
+  grid_launch_dependents();
+  grid_wait();
+  uint64_t acc[kSumAccs][4] = {};
+  constexpr int kStep = 2 * (kSumThreads / 32);
   if (col < n) {
-#pragma unroll 4
-    for (int64_t r = y; r < rows; r += kSumRows) {
-      float v[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(g + r * ldg + col)), v);
+    for (int64_t r = r0 + 2 * warp + sub; r < r1; r += kSumLoads * kStep) {
+      uint4 q[kSumLoads];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += v[i];
+      for (int j = 0; j < kSumLoads; ++j)
+        q[j] = r + j * kStep < r1 ? ld_stream(g + (r + j * kStep) * ldg + col) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < kSumLoads; ++j) {
+        const uint32_t word[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[j % kSumAccs][i] = f2_add(acc[j % kSumAccs][i],
+                                       f2_pack(__uint_as_float(word[i] << 16), __uint_as_float(word[i] & 0xffff0000u)));
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) part[y][8 * x + i] = acc[i];
-  for (int half = kSumRows / 2; half > 0; half >>= 1) {
-    __syncthreads();
-    if (y < half)
+  for (int half = kSumAccs / 2; half > 0; half >>= 1)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) part[y][8 * x + i] += part[y + half][8 * x + i];
+    for (int j = 0; j < half; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = f2_add(acc[j][i], acc[j + half][i]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    f2_unpack(acc[0][i], a, b);
+    a += __shfl_xor_sync(0xffffffffu, a, 16);
+    b += __shfl_xor_sync(0xffffffffu, b, 16);
+    if (sub == 0) {
+      part[warp][8 * lane + 2 * i] = a;
+      part[warp][8 * lane + 2 * i + 1] = b;
+    }
   }
-  if (y == 0 && col < n)
+  for (int half = kSumThreads / 64; half > 0; half >>= 1) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < half * kSumCols; i += kSumThreads)
+      part[i / kSumCols][i % kSumCols] += part[i / kSumCols + half][i % kSumCols];
+  }
+  cluster_sync();
+  if (rank == 0 && threadIdx.x < kSumCols && strip * kSumCols + static_cast<int>(threadIdx.x) < n) {
+    float v[kSumSplit];
+    const uint32_t at = smem_u32(&part[0][threadIdx.x]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dbias[col + i] += part[0][8 * x + i];
+    for (int i = 0; i < kSumSplit; ++i) v[i] = i < split ? __uint_as_float(ld_cluster_u32(cluster_map(at, i))) : 0.f;
+#pragma unroll
+    for (int half = kSumSplit / 2; half > 0; half >>= 1)
+#pragma unroll
+      for (int i = 0; i < half; ++i) v[i] += v[i + half];
+    dbias[strip * kSumCols + threadIdx.x] += v[0];
+  }
+  cluster_sync();                          // the other blocks' sums have been read
 }
 
 }  // namespace
+
+cudaError_t plan_linear_bf16(int mode, LinearParams& p) {
+  switch (mode) {
+    case kLinearFwd: return plan_mode<kLinearFwd>(p);
+    case kLinearDgrad: return plan_mode<kLinearDgrad>(p);
+    default: return plan_mode<kLinearWgrad>(p);
+  }
+}
 
 cudaError_t launch_linear_bf16(int mode, const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
   switch (mode) {
@@ -802,9 +882,15 @@ cudaError_t launch_linear_gemv(const LinearParams& p, const void* x, int64_t ldx
 }
 
 cudaError_t launch_colsum_bf16(const void* g, int64_t ldg, int rows, int n, float* dbias, cudaStream_t s) {
-  colsum_bf16_kernel<<<(n + kSumCols - 1) / kSumCols, kSumRows * kSumCols / 8, 0, s>>>(
-      static_cast<const __nv_bfloat16*>(g), ldg, rows, n, dbias);
-  return cudaGetLastError();
+  const int strips = (n + kSumCols - 1) / kSumCols;
+  // one wave (three blocks an SM), and rows for every load of a block
+  int split = 456 / strips;
+  split = split > kSumSplit ? kSumSplit : split;
+  if (split > rows / (kSumLoads * 16)) split = rows / (kSumLoads * 16);
+  if (split < 1) split = 1;
+  return launch_overlapped(colsum_bf16_kernel, static_cast<unsigned>(strips * split),
+                           kSumThreads, 0, static_cast<unsigned>(split), s, static_cast<const __nv_bfloat16*>(g), ldg,
+                           rows, n, split, dbias);
 }
 
 }  // namespace seqattn
