@@ -525,70 +525,74 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// What the device runs at once, looked up once per device: CTA pairs, and
-// clusters of each size (one CTA per SM; SMs of a group that a whole cluster
-// does not fill stay out, so 48 clusters of 3 do not fit on 152 SMs).
+// How many clusters of each size a kernel's launch has on the device at once,
+// looked up once per device and kernel.  The SMs of a group that a whole
+// cluster does not fill stay out (48 clusters of 3 CTAs do not fit on 152 SMs at
+// one CTA per SM), and a grid that passes the number by one takes twice as long.
 constexpr int kMaxDevices = 64;
 struct Residency {
-  std::atomic<int> pairs{0};
-  std::atomic<int> clusters[kMaxSplit + 1] = {};
+  std::atomic<int> ready{0};
+  std::atomic<int> fit[kMaxSplit + 1] = {};
+  int operator[](int c) const { return fit[c].load(std::memory_order_relaxed); }
 };
-Residency g_resident[kMaxDevices];
 
-template <int kMode, bool kPair>
-cudaError_t max_clusters(int cluster, int* count) {
-  auto* kernel = linear_bf16_kernel<kMode, kPair>;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(cluster) * 256u);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemAlloc;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(count, kernel, &cfg);
-}
-
-template <int kMode>
-cudaError_t residency(Residency** out) {
+template <typename... Params>
+cudaError_t look_up(void (*kernel)(Params...), unsigned threads, size_t smem, Residency (&table)[kMaxDevices],
+                    const Residency** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  Residency& r = g_resident[dev];
+  Residency& r = table[dev];
   *out = &r;
-  if (r.pairs.load(std::memory_order_acquire) > 0) return cudaSuccess;
-  int n = 0;
+  if (r.ready.load(std::memory_order_acquire)) return cudaSuccess;
+  if (smem > 0 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            static_cast<int>(smem))) != cudaSuccess)
+    return e;
   for (int c = 1; c <= kMaxSplit; ++c) {
-    if ((e = max_clusters<kMode, false>(c, &n)) != cudaSuccess) return e;
-    r.clusters[c].store(n, std::memory_order_relaxed);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(c) * 256u);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+    r.fit[c].store(n, std::memory_order_relaxed);
   }
-  if ((e = max_clusters<kMode, true>(2, &n)) != cudaSuccess) return e;
-  if (n < 1 || r.clusters[1].load(std::memory_order_relaxed) < 1) return cudaErrorLaunchOutOfResources;
-  r.pairs.store(n, std::memory_order_release);
+  r.ready.store(1, std::memory_order_release);
   return cudaSuccess;
+}
+
+// The largest cluster, up to `most`, with which `count` clusters run at once (1 if none).
+int widest_cluster(const Residency& r, int count, int64_t most) {
+  int c = most < kMaxSplit ? static_cast<int>(most) : kMaxSplit;
+  while (c > 1 && r[c] < count) --c;
+  return c < 1 ? 1 : c;
 }
 
 // Chooses the shape for p.m x p.n with contraction p.k: the one, and the tile
 // width or split, whose waves of tiles take the least time in the cost model.
 template <int kMode>
 cudaError_t plan_mode(LinearParams& p) {
-  cudaError_t e = cudaFuncSetAttribute(linear_bf16_kernel<kMode, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSmemAlloc);
+  static Residency pair_table[kMaxDevices], split_table[kMaxDevices];
+  const Residency *pair_fit = nullptr, *split_fit = nullptr;
+  cudaError_t e = look_up(linear_bf16_kernel<kMode, true>, kThreads, kSmemAlloc, pair_table, &pair_fit);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(linear_bf16_kernel<kMode, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
-  if (e != cudaSuccess) return e;
-  Residency* res = nullptr;
-  if ((e = residency<kMode>(&res)) != cudaSuccess) return e;
+  if ((e = look_up(linear_bf16_kernel<kMode, false>, kThreads, kSmemAlloc, split_table, &split_fit)) != cudaSuccess)
+    return e;
+  const int pairs = (*pair_fit)[2];
+  if (pairs < 1 || (*split_fit)[1] < 1) return cudaErrorLaunchOutOfResources;
   const int64_t stages = (static_cast<int64_t>(p.k) + kTK - 1) / kTK;
   p.a_bytes = kMode == kLinearWgrad ? kOperandBytes : static_cast<uint32_t>(linear_a_rows(p.m) * kTK * 2);
   int64_t best = INT64_MAX;
   // a pair copies whole tiles of A, so a result of fewer rows is left to the split shape
   if (p.a_bytes == kOperandBytes) {
-    const int pairs = res->pairs.load(std::memory_order_relaxed);
     // widths: wgrad's epilogue adds 32-column boxes of a half; a forward whose
     // W comes in whole blocks (see load_tile) would lose that with halves that
     // are not (2048 x 4096 x 4096 with 240 columns: 62 us, 50 with 256)
@@ -607,7 +611,7 @@ cudaError_t plan_mode(LinearParams& p) {
   }
   const int64_t small = static_cast<int64_t>((p.m + 127) / 128) * ((p.n + 127) / 128);
   for (int c = 1; c <= kMaxSplit && c <= stages; ++c) {
-    const int fit = res->clusters[c].load(std::memory_order_relaxed);
+    const int fit = (*split_fit)[c];
     if (fit < 1 || small > INT32_MAX / kMaxSplit) continue;
     const int64_t cost = ((small + fit - 1) / fit) * ((stages + c - 1) / c * kSplitStageCost + kSplitFixedCost) +
                          (c - 1) * kSplitJoinCost;
@@ -758,14 +762,14 @@ __global__ void __launch_bounds__(kGvThreads)
 
 template <int R, int kCols>
 cudaError_t gemv_strips(LinearParams p, const void* x, int64_t ldx, const void* w, cudaStream_t s) {
+  static Residency table[kMaxDevices];
+  const Residency* fit = nullptr;
+  const cudaError_t e = look_up(linear_gemv_kernel<R, kCols>, kGvThreads, 0, table, &fit);
+  if (e != cudaSuccess) return e;
   const int strips = (p.n + kCols - 1) / kCols;
-  // blocks enough for about two per SM, each with at least 64 rows of W
-  int split = (304 + strips - 1) / strips;
-  split = split > 8 ? 8 : split;
-  while (split > 1 && p.k / split < 64) --split;
-  p.split = split;
-  return launch_overlapped(linear_gemv_kernel<R, kCols>, static_cast<unsigned>(strips * split), kGvThreads, 0,
-                           static_cast<unsigned>(split), s, p, static_cast<const __nv_bfloat16*>(x), ldx,
+  p.split = widest_cluster(*fit, strips, p.k / 64);      // each block at least 64 rows of W
+  return launch_overlapped(linear_gemv_kernel<R, kCols>, static_cast<unsigned>(strips) * p.split, kGvThreads, 0,
+                           static_cast<unsigned>(p.split), s, p, static_cast<const __nv_bfloat16*>(x), ldx,
                            static_cast<const __nv_bfloat16*>(w));
 }
 
@@ -790,7 +794,7 @@ constexpr int kSumThreads = 256;
 constexpr int kSumCols = 128;
 constexpr int kSumLoads = 8;        // loads in flight per lane
 constexpr int kSumAccs = 4;         // sums per lane and column
-constexpr int kSumSplit = 8;
+constexpr int kSumSplit = kMaxSplit;
 
 __global__ void __launch_bounds__(kSumThreads, 3)
     colsum_bf16_kernel(const __nv_bfloat16* __restrict__ g, int64_t ldg, int rows, int n, int split,
@@ -882,12 +886,12 @@ cudaError_t launch_linear_gemv(const LinearParams& p, const void* x, int64_t ldx
 }
 
 cudaError_t launch_colsum_bf16(const void* g, int64_t ldg, int rows, int n, float* dbias, cudaStream_t s) {
+  static Residency table[kMaxDevices];
+  const Residency* fit = nullptr;
+  const cudaError_t e = look_up(colsum_bf16_kernel, kSumThreads, 0, table, &fit);
+  if (e != cudaSuccess) return e;
   const int strips = (n + kSumCols - 1) / kSumCols;
-  // one wave (three blocks an SM), and rows for every load of a block
-  int split = 456 / strips;
-  split = split > kSumSplit ? kSumSplit : split;
-  if (split > rows / (kSumLoads * 16)) split = rows / (kSumLoads * 16);
-  if (split < 1) split = 1;
+  const int split = widest_cluster(*fit, strips, rows / (kSumLoads * 16));     // rows for every load of a block
   return launch_overlapped(colsum_bf16_kernel, static_cast<unsigned>(strips * split),
                            kSumThreads, 0, static_cast<unsigned>(split), s, static_cast<const __nv_bfloat16*>(g), ldg,
                            rows, n, split, dbias);
