@@ -88,7 +88,8 @@ struct LinearBarriers {
 };
 
 // ---- activations (z in float32) -------------------------------------------
-__device__ __forceinline__ float sigmoidf(float z) { return 1.f / (1.f + __expf(-z)); }
+// (fast exponential and quotient: a few 2^-22 of a value that is rounded to bf16)
+__device__ __forceinline__ float sigmoidf(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 constexpr float kTanhA = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float kTanhB = 0.044715f;
 
@@ -169,16 +170,66 @@ __device__ __forceinline__ void finish8(const LinearParams& p, int64_t row, int 
   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * p.ldo + col) = pack8(v);
 }
 
-// 32 consecutive columns of one row, those below `end`.
+// 32 x 32 of the result: this lane's row of it in `acc`, rows from row0 and
+// columns from col on, those below p.m and `end`.  The warp turns the block
+// around in its shared-memory box (4 KB, 128-byte rows, 16-byte chunks XORed
+// with the row), so that four lanes finish a row's 32 columns side by side:
+// eight rows of 64 contiguous bytes an access instead of 32 rows of 16.
 template <int kMode, int kAct>
-__device__ __forceinline__ void finish32(const LinearParams& p, int64_t row, int col, int end, const float (&r)[32]) {
+__device__ __forceinline__ void finish_block(const LinearParams& p, uint8_t* box, int row0, int col, int end,
+                                             const uint32_t (&acc)[32]) {
+  const int lane = lane_id();
+  __syncwarp();                                  // the previous block has been read
 #pragma unroll
-  for (int j = 0; j < 32; j += 8) {
-    if (col + j >= end) break;
-    float v[8];
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+        make_uint4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+  __syncwarp();
+  const int q = lane & 3, c = col + 8 * q;
+  if (c >= end) return;
+  float bias[8] = {};
+  if (kMode == kLinearFwd && p.bias != nullptr) unpack8(__ldg(reinterpret_cast<const uint4*>(p.bias + c)), bias);
+  constexpr int kAhead = 2;                      // rows whose z and residual are loaded together
+#pragma unroll 1
+  for (int i0 = 0; i0 < 4; i0 += kAhead) {
+    uint4 zin[kAhead], res[kAhead];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = r[j + i];
-    finish8<kMode, kAct>(p, row, col + j, v);
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t row = row0 + 8 * (i0 + i) + (lane >> 2);
+      if (row >= p.m) break;
+      if constexpr (kMode == kLinearDgrad && kAct != kActNone)
+        zin[i] = *reinterpret_cast<const uint4*>(p.z + row * p.ldz + c);
+      if (p.residual != nullptr) res[i] = *reinterpret_cast<const uint4*>(p.residual + row * p.ldr + c);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = 8 * (i0 + i) + (lane >> 2);
+      const int64_t row = row0 + r;
+      if (row >= p.m) break;
+      float v[8], t[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 x = *reinterpret_cast<const float4*>(box + r * 128 + (((2 * q + h) ^ (r & 7)) << 4));
+        v[4 * h] = x.x, v[4 * h + 1] = x.y, v[4 * h + 2] = x.z, v[4 * h + 3] = x.w;
+      }
+      if constexpr (kMode == kLinearFwd) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += bias[k];
+        if (p.z != nullptr) *reinterpret_cast<uint4*>(p.z + row * p.ldz + c) = pack8(v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = act_value<kAct>(v[k]);
+      } else if constexpr (kAct != kActNone) {
+        unpack8(zin[i], t);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= act_grad<kAct>(t[k]);
+      }
+      if (p.residual != nullptr) {
+        unpack8(res[i], t);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += t[k];
+      }
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * p.ldo + c) = pack8(v);
+    }
   }
 }
 
@@ -397,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile_row = (kPair ? 128 * static_cast<int>(rank) : 0) + quad * 32 + lane;
     const uint32_t leader_empty[2] = {cluster_map(smem_u32(&bars.acc_empty[0]), kPair ? 0 : rank),
                                       cluster_map(smem_u32(&bars.acc_empty[1]), kPair ? 0 : rank)};
+    uint8_t* box = smem + kOffBox + (warp - 2) * kBoxBytes;    // this warp's 4 KB
     int c = 0;
     bool ok = true;
     for (int t = first_tile; ok && t < n_tiles; t += tile_step) {
@@ -427,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kPair) {
           // dw += the tile, 32 x 32 at a time through this warp's box: TMA adds
           // it in L2 (float32, one addition an element), clipped at dw's edges
-          uint8_t* box = smem + kOffBox + (warp - 2) * kBoxBytes;
           const int row0 = static_cast<int>(row) - lane;
 #pragma unroll
           for (int c0 = 0; c0 < S::kColsPerWarp; c0 += 32) {
@@ -461,10 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t r[32];
             tmem_ld32(my_cols + static_cast<uint32_t>((c & 1) * S::kTN + c0), r);
             tmem_ld_wait();
-            float f[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]);
-            if (row < p.m) finish32<kMode, decltype(act)::value>(p, row, col + c0, min(p.n, col + warp_cols), f);
+            finish_block<kMode, decltype(act)::value>(p, box, static_cast<int>(row) - lane, col + c0,
+                                                      min(p.n, col + warp_cols), r);
           }
         });
         tc_fence_before_sync();
