@@ -737,3 +737,135 @@ def test_adamw_refuses():
     with pytest.raises(binding.SeqattnError, match="aligned"):
         binding.AdamW([torch.zeros(301, device="cuda")[1:]], g).step(1e-3, 1)
     binding.AdamW([], []).step(1e-3, 1)
+
+
+# ============================================================== offsets past 32 bits
+
+def test_norm_rope_in_a_cache_of_more_than_2_31_elements():
+    """Rows near the end of 4.4 GB caches: the same bits as the same rows of a
+    short cache, given the same positions."""
+    B, c, Hq, Hkv, d, T = 1, 3, 64, 64, 128, 270000
+    start = T - c
+    assert start * Hkv * d > 2 ** 31
+    qkv = _rand(110, B, c, Hq + 2 * Hkv, d).cuda()
+    q_in, k_in, v_in = qkv.split((Hq, Hkv, Hkv), 2)
+    gamma = (1 + _rand(111, d, dtype=torch.float32, std=0.2)).bfloat16().cuda()
+    plan = binding.rope_plan([1e4 ** (-i / 64) for i in range(64)])
+    pos = torch.arange(start, T, device="cuda")[None, None]
+    outs = []
+    for rows, at, p in ((T, start, None), (c, 0, pos)):
+        q = torch.zeros((B, c, Hq, d), dtype=torch.bfloat16, device="cuda")
+        k = torch.zeros((B, rows, Hkv, d), dtype=torch.bfloat16, device="cuda")
+        v = torch.zeros_like(k)
+        binding.qk_norm_rope_fwd(q_in, k_in, v_in, q, k, v, at, gamma_q=gamma, gamma_k=gamma, plan=plan, positions=p)
+        assert int((k[:, :at] != 0).sum()) == 0 and int((v[:, :at] != 0).sum()) == 0
+        outs.append((q, k[:, at:].clone(), v[:, at:].clone()))
+        del k, v
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    dq = _rand(112, B, c, Hq, d, dtype=torch.float32).cuda()
+    rows_dk = _rand(113, B, c, Hkv, d, dtype=torch.float32).cuda()
+    outs = []
+    for rows, at, p in ((T, start, None), (c, 0, pos)):
+        dk = torch.empty((B, rows, Hkv, d), device="cuda")
+        dk[:, at:] = rows_dk
+        dx, dgq, dgk = torch.zeros_like(qkv), torch.zeros(d, device="cuda"), torch.zeros(d, device="cuda")
+        oq, ok, _ = dx.split((Hq, Hkv, Hkv), 2)
+        binding.qk_norm_rope_bwd(q_in, k_in, dq, dk, None, oq, ok, None, at, gamma_q=gamma, gamma_k=gamma,
+                                 dgamma_q=dgq, dgamma_k=dgk, plan=plan, positions=p)
+        outs.append((dx, dgq, dgk))
+        del dk
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_linear_with_more_than_2_31_elements():
+    rows, k, n = 270000, 64, 8192
+    x, w = _rand(114, 4096, k).cuda().repeat(66, 1)[:rows], _rand(115, k, n).cuda()
+    y = torch.empty((rows, n), dtype=torch.bfloat16, device="cuda")
+    binding.linear_fwd(x, w, y)
+    ref = x[:4096].double() @ w.double()
+    tol = U_BF16 * ref.abs() + _sum_tol(k, x[:4096].double().abs() @ w.double().abs())
+    for at in (0, 4096 * 63, 4096 * 64):
+        off = (y[at:at + 4096].double() - ref).abs()
+        assert bool((off <= tol).all())
+    assert torch.equal(y[4096 * 65:], y[:rows - 4096 * 65])
+    dx = torch.empty_like(x)
+    binding.linear_dgrad(y, w, dx)                      # reads the long matrix
+    assert torch.equal(dx[4096 * 64:4096 * 65], dx[:4096])
+    assert torch.equal(dx[4096 * 65:], dx[:rows - 4096 * 65])
+    dw, part = torch.zeros((k, n), device="cuda"), torch.zeros((k, n), device="cuda")
+    tail = rows - 4096 * 65
+    y[:rows - tail] = 0                                 # only the last rows count
+    binding.linear_wgrad(x, y, dw)
+    binding.linear_wgrad(x[rows - tail:], y[rows - tail:], part)
+    mags = x[rows - tail:].double().abs().t() @ y[rows - tail:].double().abs()
+    _within("dw", dw, part.double().cpu(), 2 * (48 * 2.0 ** -23 + (rows / 512 + 2) * U_F32) * mags.cpu())
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_tensor_of_more_than_2_31_elements(bits):
+    n, cut = 2 ** 31 + 256 * 5 + 77, 2 ** 31 - 256
+    tail_p = _rand(116, n - cut, dtype=torch.float32).cuda()
+    tail_g = _rand(117, n - cut).cuda()
+    p = torch.zeros(n, device="cuda")
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    p[cut:], g[cut:] = tail_p, tail_g
+    big, small = binding.AdamW([p], [g], state_bits=bits), binding.AdamW([tail_p], [tail_g], state_bits=bits)
+    for step in (1, 2):
+        big.step(1e-2, step)
+        small.step(1e-2, step)
+    torch.cuda.synchronize()
+    assert torch.equal(p[cut:], tail_p) and int((p[:cut] != 0).sum()) == 0
+    assert torch.equal(big.m[0][cut:].float(), small.m[0].float())
+    assert torch.equal(big.v[0][cut:].float(), small.v[0].float())
+    if bits == 8:
+        assert torch.equal(big.m_scale[0][cut // 256:], small.m_scale[0])
+
+
+# ============================================================== side by side
+
+def test_all_operators_on_two_streams_at_once():
+    """Two streams run the same chain of different data over shared weights,
+    several times; each gets what it gets alone."""
+    k, n, rows, H, d = 512, 6 * 64, 300, 2, 64
+    w = _rand(120, k, n, std=k ** -0.5).cuda()
+    gamma = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    plan = binding.rope_plan([1e4 ** (-i / 32) for i in range(32)])
+
+    def state(seed):
+        z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt, device="cuda")        # noqa: E731
+        return dict(x=_rand(seed, rows, k).cuda(), qkv=z(rows, n, dt=torch.bfloat16),
+                    q=z(1, rows, H, d, dt=torch.bfloat16), k=z(1, rows, H, d, dt=torch.bfloat16),
+                    v=z(1, rows, H, d, dt=torch.bfloat16), dq=_rand(seed + 1, 1, rows, H, d, dtype=torch.float32).cuda(),
+                    dx=z(1, rows, 3 * H, d, dt=torch.bfloat16), dh=z(rows, k, dt=torch.bfloat16), dw=z(k, n),
+                    db=z(n), dgq=z(d), dgk=z(d), p=z(k, n))
+
+    def chain(s, opt, stream):
+        with torch.cuda.stream(stream):
+            for t in (s["dw"], s["db"], s["dgq"], s["dgk"]):
+                t.zero_()
+            binding.linear_fwd(s["x"], w, s["qkv"])
+            q_in, k_in, v_in = s["qkv"].view(1, rows, 3 * H, d).split((H, H, H), 2)
+            binding.qk_norm_rope_fwd(q_in, k_in, v_in, s["q"], s["k"], s["v"], 0, gamma_q=gamma, gamma_k=gamma, plan=plan)
+            oq, ok, ov = s["dx"].split((H, H, H), 2)
+            binding.qk_norm_rope_bwd(q_in, k_in, s["dq"], s["dq"], s["dq"], oq, ok, ov, 0, gamma_q=gamma, gamma_k=gamma,
+                                     dgamma_q=s["dgq"], dgamma_k=s["dgk"], plan=plan)
+            flat = s["dx"].view(rows, n)
+            binding.linear_dgrad(flat, w, s["dh"])
+            binding.linear_wgrad(s["x"], flat, s["dw"], dbias=s["db"])
+            opt.step(1e-2, 1)
+
+    def run(streams):
+        states = [state(130), state(140)]
+        opts = [binding.AdamW([s["p"]], [s["dw"]], state_bits=8) for s in states]
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for s, o, st in zip(states, opts, streams):
+                chain(s, o, st)
+        torch.cuda.synchronize()
+        return states
+
+    main = torch.cuda.current_stream()
+    alone, together = run([main, main]), run([torch.cuda.Stream(), torch.cuda.Stream()])
+    for a, b in zip(alone, together):
+        for name in a:
+            assert torch.equal(a[name], b[name]), name
