@@ -1,8 +1,9 @@
 """ctypes binding of libseqattn (include/seqattn.h).
 
 Every step of the computation runs in the library's CUDA kernels.  The call
-wrappers turn torch tensors into device pointers and sizes, pass the torch
-CUDA stream, and raise ``SeqattnError`` on a non-OK status.  The layer drivers
+wrappers turn torch tensors into device pointers and sizes (those of the
+layer's short operators in C++, csrc/marshal.cpp), pass the torch CUDA stream,
+and raise ``SeqattnError`` on a non-OK status.  The layer drivers
 below them (``forward_chunks``, ``backward_chunks``, ``layer_forward_backward``,
 ``LayerGraph``, ``HostLayerPass``) are host logic only: they order the chunk
 calls over CUDA streams and events, and do no arithmetic.  If the library has
@@ -306,85 +307,32 @@ def _act_code(act):
     return ACTIVATIONS[act]
 
 
-# These calls are short on the device, so the checks are written for the usual
-# case: one look at each tensor's type, device, shape and strides (about 0.5 us
-# a tensor), and the words of a refusal are put together only when it is due.
+# These calls are short on the device, so their tensors are checked and turned
+# into pointers and strides in C++ (csrc/marshal.cpp), by position.
 
 _bf16 = torch.bfloat16
 _f32 = torch.float32
+_marshal = None
+
+
+def _native():
+    """The compiled argument checks (loaded once, after the library)."""
+    global _marshal
+    if _marshal is None:
+        load_library()
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise RuntimeError("_marshal.so is not built for this PyTorch; run "
+                               "long_context_attention_seqattn_gb300.build.build()") from e
+        _marshal = m
+    return _marshal
 
 
 def _refuse(t, name, dtype):
     if not t.is_cuda or t.dtype != dtype:
         raise ValueError(f"{name} must be a CUDA tensor of {dtype}")
     raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-
-
-def _device(t, name, dtype):
-    """Index of the current device, for a call whose first tensor is ``t``."""
-    if t.get_device() < 0:
-        _refuse(t, name, dtype)
-    return torch._C._cuda_getDevice()
-
-
-def _raw_stream(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _matrix(t, name, cols, rows, dev, dtype=_bf16):
-    """(rows, row stride) of a tensor seen as a matrix of its last dimension;
-    the leading dimensions must lie at one uniform row stride."""
-    if t.dtype is not dtype or t.get_device() != dev:
-        _refuse(t, name, dtype)
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 2:
-        r, c = shape
-        ld = stride[0] if r > 1 else c
-    elif len(shape) < 2:
-        raise ValueError(f"{name} must have at least two dimensions")
-    else:
-        r, c, ld = 1, shape[-1], None
-        for size, st in zip(reversed(shape[:-1]), reversed(stride[:-1])):
-            if size == 1:
-                continue
-            if ld is None:
-                ld = st
-            elif st != r * ld and size * r:
-                raise ValueError(f"the rows of {name} must lie at one uniform stride")
-            r *= size
-        if ld is None or r <= 1:
-            ld = c
-    if stride[-1] != 1 and c > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    if c != cols:
-        raise ValueError(f"{name} has {c} columns, expected {cols}")
-    if rows is not None and r != rows:
-        raise ValueError(f"{name} has {r} rows, expected {rows}")
-    return r, ld
-
-
-def _weight(w, dev):
-    if w.dtype is not _bf16 or w.get_device() != dev:
-        _refuse(w, "w", _bf16)
-    if w.dim() != 2 or not w.is_contiguous():
-        raise ValueError("w must be a contiguous [k, n] matrix")
-    return w.shape
-
-
-def _vector(t, name, n, dtype, dev):
-    if t.dtype is not dtype or t.get_device() != dev:
-        _refuse(t, name, dtype)
-    if t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous vector of {n} elements")
-    return t.data_ptr()
-
-
-def _dense(t, name, shape, dtype, dev):
-    if t.dtype is not dtype or t.get_device() != dev:
-        _refuse(t, name, dtype)
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, not {tuple(t.shape)}")
-    return t.data_ptr()
 
 
 def _addr(t):
@@ -396,19 +344,9 @@ def linear_fwd(x, w, y, bias=None, act="none", residual=None, z=None, stream=Non
     ``y``, ``residual`` [..., n] bf16 with rows at a uniform stride, ``w``
     [k, n] and ``bias`` [n] bf16.  ``z`` [..., n] bf16, if given, receives the
     pre-activation x w + bias.  ``residual`` may be ``y``."""
-    dev = _device(w, "w", _bf16)
-    k, n = _weight(w, dev)
-    rows, ldx = _matrix(x, "x", k, None, dev)
-    _, ldy = _matrix(y, "y", n, rows, dev)
-    ldr = ldz = 0
-    b = None if bias is None else _vector(bias, "bias", n, _bf16, dev)
-    if residual is not None:
-        _, ldr = _matrix(residual, "residual", n, rows, dev)
-    if z is not None:
-        _, ldz = _matrix(z, "z", n, rows, dev)
-    _check((_lib or load_library()).seqattn_linear_fwd(
-        rows, k, n, x.data_ptr(), ldx, w.data_ptr(), b, _act_code(act), _addr(residual), ldr, _addr(z), ldz,
-        y.data_ptr(), ldy, _raw_stream(stream, dev)))
+    status = (_marshal or _native()).linear_fwd(x, w, y, bias, _act_code(act), residual, z, stream)
+    if status:
+        _check(status)
 
 
 def linear_dgrad(g, w, dx, act="none", z=None, residual=None, stream=None):
@@ -418,21 +356,9 @@ def linear_dgrad(g, w, dx, act="none", z=None, residual=None, stream=None):
     ``linear_fwd`` of the layer before kept it).  ``g`` [..., n], ``dx``,
     ``z``, ``residual`` [..., k] bf16, ``w`` [k, n].  ``residual`` may be
     ``dx`` (several gradients of one input are summed that way)."""
-    dev = _device(w, "w", _bf16)
-    k, n = _weight(w, dev)
-    code = _act_code(act)
-    rows, ldg = _matrix(g, "g", n, None, dev)
-    _, lddx = _matrix(dx, "dx", k, rows, dev)
-    ldr = ldz = 0
-    if residual is not None:
-        _, ldr = _matrix(residual, "residual", k, rows, dev)
-    if code:
-        if z is None:
-            raise ValueError("z is needed when act is given")
-        _, ldz = _matrix(z, "z", k, rows, dev)
-    _check((_lib or load_library()).seqattn_linear_dgrad(
-        rows, k, n, g.data_ptr(), ldg, w.data_ptr(), code, z.data_ptr() if code else None, ldz, _addr(residual), ldr,
-        dx.data_ptr(), lddx, _raw_stream(stream, dev)))
+    status = (_marshal or _native()).linear_dgrad(g, w, dx, _act_code(act), z, residual, stream)
+    if status:
+        _check(status)
 
 
 def linear_wgrad(x, g, dw, dbias=None, stream=None):
@@ -440,14 +366,9 @@ def linear_wgrad(x, g, dw, dbias=None, stream=None):
     [..., n] bf16 with rows at a uniform stride, ``dw`` [k, n] and ``dbias``
     [n] float32, accumulated.  (``proj_wgrad`` is the form for float32 g of
     whole [B, T, ...] gradients.)"""
-    dev = _device(x, "x", _bf16)
-    k, n = x.shape[-1], g.shape[-1]
-    rows, ldx = _matrix(x, "x", k, None, dev)
-    _, ldg = _matrix(g, "g", n, rows, dev)
-    w = _dense(dw, "dw", (k, n), _f32, dev)
-    b = None if dbias is None else _vector(dbias, "dbias", n, _f32, dev)
-    _check((_lib or load_library()).seqattn_linear_wgrad(rows, k, n, x.data_ptr(), ldx, g.data_ptr(), ldg, w, b,
-                                                         _raw_stream(stream, dev)))
+    status = (_marshal or _native()).linear_wgrad(x, g, dw, dbias, stream)
+    if status:
+        _check(status)
 
 
 def rope_plan(inv_freq, axis=None, interleaved=False):
@@ -476,31 +397,6 @@ def rope_plan(inv_freq, axis=None, interleaved=False):
 _TWO_PI = Fraction(6283185307179586476925286766559005768394, 10 ** 39)
 
 
-def _head_rows(t, name, shape, dtype, dev):
-    """Row stride of a [B, c, H, d] tensor whose heads are dense and whose rows
-    (b, r) lie at one uniform stride."""
-    if t.dtype is not dtype or t.get_device() != dev:
-        _refuse(t, name, dtype)
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    B, c, H, d = shape
-    sb, sc, sh, sd = t.stride()
-    if sd != 1 or (sh != d and H > 1):
-        raise ValueError(f"the heads of {name} must be dense")
-    if c > 1:
-        if B > 1 and sb != c * sc:
-            raise ValueError(f"the rows of {name} must lie at one uniform stride")
-        return sc
-    return sb if B > 1 and c == 1 else H * d
-
-
-def _rope_positions(positions, plan, B, c, dev):
-    axes = plan.axes if plan is not None else 1
-    if positions.dim() == 2 and axes == 1:
-        positions = positions[None]
-    return _dense(positions, "positions", (axes, B, c), torch.int64, dev)
-
-
 def qk_norm_rope_fwd(q_in, k_in, v_in, q, k_cache, v_cache, q_start, gamma_q=None, gamma_k=None, eps=1e-6,
                      plan=None, positions=None, stream=None):
     """From the projections to the attention, for the chunk whose rows are
@@ -512,39 +408,14 @@ def qk_norm_rope_fwd(q_in, k_in, v_in, q, k_cache, v_cache, q_start, gamma_q=Non
     may be parts of a fused projection's output (dense heads, uniform row
     stride); ``v_in`` and ``v_cache`` may both be None.  ``positions``: int64
     [axes, B, c] (or [B, c]); by default row r is at position q_start + r."""
-    dt = q.dtype
-    dev = _device(q, "q", dt)
-    B, c, Hq, d = q.shape
-    cache = k_cache.shape
-    Hkv = cache[2]
-    if len(cache) != 4 or cache[0] != B or cache[3] != d:
-        raise ValueError(f"a cache of shape {tuple(cache)} does not go with queries of shape {tuple(q.shape)}")
-    if (v_in is None) != (v_cache is None):
-        raise ValueError("v_in and v_cache must both be given or both be None")
-    if (gamma_q is None) != (gamma_k is None):
-        raise ValueError("gamma_q and gamma_k must both be given or both be None")
-    heads = (B, c, Hkv, d)
-    ldq = _head_rows(q_in, "q_in", (B, c, Hq, d), dt, dev)
-    ldk = _head_rows(k_in, "k_in", heads, dt, dev)
-    ldv, v_src, v_dst, gq, gk = 0, None, None, None, None
-    if v_in is not None:
-        ldv, v_src = _head_rows(v_in, "v_in", heads, dt, dev), v_in.data_ptr()
-        v_dst = _dense(v_cache, "v_cache", cache, dt, dev)
-    if gamma_q is not None:
-        gq, gk = _vector(gamma_q, "gamma_q", d, dt, dev), _vector(gamma_k, "gamma_k", d, dt, dev)
-    _check((_lib or load_library()).seqattn_qk_norm_rope_fwd(
-        Problem(B, Hq, Hkv, d, cache[1], _dtype_code(dt)), q_start, c, q_in.data_ptr(), ldq, k_in.data_ptr(), ldk,
-        v_src, ldv, gq, gk, eps, plan,
-        None if positions is None else _rope_positions(positions, plan, B, c, dev),
-        _dense(q, "q", q.shape, dt, dev), _dense(k_cache, "k_cache", cache, dt, dev), v_dst,
-        _raw_stream(stream, dev)))
+    status = (_marshal or _native()).norm_rope_fwd(q_in, k_in, v_in, q, k_cache, v_cache, q_start, gamma_q, gamma_k,
+                                                   eps, plan, positions, stream)
+    if status:
+        _check(status)
 
 
 def qk_norm_rope_bwd_workspace_size(head_dim):
     return int(load_library().seqattn_qk_norm_rope_bwd_workspace_size(Problem(1, 1, 1, head_dim, 1, SEQATTN_BF16)))
-
-
-_rope_ws_bytes = {}      # head_dim -> bytes
 
 
 def qk_norm_rope_bwd(q_in, k_in, dq, dk_accum, dv_accum, dq_in, dk_in, dv_in, q_start, gamma_q=None, gamma_k=None,
@@ -558,48 +429,15 @@ def qk_norm_rope_bwd(q_in, k_in, dq, dk_accum, dv_accum, dq_in, dk_in, dv_in, q_
     float32 are accumulated; ``workspace`` is a uint8 CUDA tensor of at least
     ``qk_norm_rope_bwd_workspace_size(d)`` bytes (allocated here when
     omitted).  ``dv_accum`` and ``dv_in`` may both be None."""
-    dt = dq_in.dtype
-    dev = _device(dq, "dq", _f32)
-    B, c, Hq, d = dq.shape
-    cache = dk_accum.shape
-    Hkv = cache[2]
-    if len(cache) != 4 or cache[0] != B or cache[3] != d:
-        raise ValueError(f"accumulators of shape {tuple(cache)} do not go with dq of shape {tuple(dq.shape)}")
-    if (dv_accum is None) != (dv_in is None):
-        raise ValueError("dv_accum and dv_in must both be given or both be None")
-    if (gamma_q is None) != (gamma_k is None):
-        raise ValueError("gamma_q and gamma_k must both be given or both be None")
-    queries, heads = (B, c, Hq, d), (B, c, Hkv, d)
-    lddq = _head_rows(dq_in, "dq_in", queries, dt, dev)
-    lddk = _head_rows(dk_in, "dk_in", heads, dt, dev)
-    lddv = ldq = ldk = ws_bytes = 0
-    v_src = v_dst = xq = xk = gq = gk = dgq = dgk = ws = None
-    if dv_in is not None:
-        lddv, v_dst = _head_rows(dv_in, "dv_in", heads, dt, dev), dv_in.data_ptr()
-        v_src = _dense(dv_accum, "dv_accum", cache, _f32, dev)
-    temp = False
-    if gamma_q is not None:
-        if dgamma_q is None or dgamma_k is None:
-            raise ValueError("dgamma_q and dgamma_k are needed with a norm")
-        ldq, xq = _head_rows(q_in, "q_in", queries, dt, dev), q_in.data_ptr()
-        ldk, xk = _head_rows(k_in, "k_in", heads, dt, dev), k_in.data_ptr()
-        gq, gk = _vector(gamma_q, "gamma_q", d, dt, dev), _vector(gamma_k, "gamma_k", d, dt, dev)
-        dgq = _vector(dgamma_q, "dgamma_q", d, _f32, dev)
-        dgk = _vector(dgamma_k, "dgamma_k", d, _f32, dev)
-        temp = workspace is None
-        if temp:
-            if d not in _rope_ws_bytes:
-                _rope_ws_bytes[d] = qk_norm_rope_bwd_workspace_size(d)
-            workspace = torch.empty(_rope_ws_bytes[d], dtype=torch.uint8, device=dq.device)
-        ws_bytes = workspace.numel()
-        ws = _dense(workspace, "workspace", workspace.shape, torch.uint8, dev)
-    _check((_lib or load_library()).seqattn_qk_norm_rope_bwd(
-        Problem(B, Hq, Hkv, d, cache[1], _dtype_code(dt)), q_start, c, xq, ldq, xk, ldk, gq, gk, eps, plan,
-        None if positions is None else _rope_positions(positions, plan, B, c, dev),
-        _dense(dq, "dq", dq.shape, _f32, dev), _dense(dk_accum, "dk_accum", cache, _f32, dev), v_src,
-        dq_in.data_ptr(), lddq, dk_in.data_ptr(), lddk, v_dst, lddv, dgq, dgk, ws, ws_bytes,
-        _raw_stream(stream, dev)))
-    if temp and stream is not None:
+    temp = workspace is None and stream is not None and gamma_q is not None
+    if temp:
+        workspace = torch.empty(qk_norm_rope_bwd_workspace_size(dq.shape[-1]), dtype=torch.uint8, device=dq.device)
+    status = (_marshal or _native()).norm_rope_bwd(q_in, k_in, dq, dk_accum, dv_accum, dq_in, dk_in, dv_in, q_start,
+                                                   gamma_q, gamma_k, dgamma_q, dgamma_k, eps, plan, positions,
+                                                   workspace, stream)
+    if status:
+        _check(status)
+    if temp:
         workspace.record_stream(stream)       # as in chunk_bwd
 
 
@@ -668,8 +506,8 @@ class AdamW:
         numbers are kept as they were at the capture."""
         if not self.params:
             return
-        dev = _device(self.params[0], "params[0]", _f32)
-        if self.params[0].get_device() != dev:
+        dev = self.device.index
+        if dev != torch._C._cuda_getDevice():
             _refuse(self.params[0], "params[0]", _f32)
         on_device = [None, None, None]
         for i, (name, value, dtype) in enumerate((("lr", lr, _f32), ("grad_scale", grad_scale, _f32),
@@ -684,7 +522,8 @@ class AdamW:
         a = AdamwParams(0.0 if lr_dev else lr, beta1, beta2, eps, 1.0 if scale_dev else grad_scale,
                         0 if step_dev else step, lr_dev, scale_dev, step_dev)
         _check((_lib or load_library()).seqattn_adamw_step(self._tensors, len(self.params), self.state_bits, a,
-                                                           _raw_stream(stream, dev)))
+                                                           torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                                                           else stream.cuda_stream))
 
 
 def sync_status(stream=None):
