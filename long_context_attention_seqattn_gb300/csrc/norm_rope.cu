@@ -193,6 +193,29 @@ __device__ __forceinline__ void stretch(int64_t total, int64_t* begin, int64_t* 
   *end = *begin + each + (w < rest ? 1 : 0);
 }
 
+// A place in the sequence: row, its row r within the batch entry, its first
+// cached element, group g; moving to the next row divides nothing.
+struct Place {
+  int64_t row, cache;
+  int r, g;
+  __device__ __forceinline__ Place(const NormRopeParams& p, const Groups& gr, int64_t at, int d) {
+    row = at / gr.all;
+    g = static_cast<int>(at - row * gr.all);
+    const int64_t b = row / p.q_len;
+    r = static_cast<int>(row - b * p.q_len);
+    cache = (b * p.T + p.q_start + r) * p.Hkv * d;
+  }
+  __device__ __forceinline__ void next_row(const NormRopeParams& p, int d) {
+    g = 0;
+    ++row;
+    cache += p.Hkv * d;
+    if (++r == p.q_len) {
+      r = 0;
+      cache += (p.T - p.q_len) * p.Hkv * d;
+    }
+  }
+};
+
 // Norm and rotation of the groups [g0, g1) of one kind (queries or keys) of a row.
 template <typename E, int D, bool kNorm, bool kInter, int U>
 __device__ __forceinline__ void fwd_heads(const NormRopeParams& p, const LaneRotation<kInter>& lr, const RowAngles& ang,
@@ -277,14 +300,11 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocksPerSm)
   grid_launch_dependents();
   grid_wait();
   stretch(static_cast<int64_t>(p.B) * p.q_len * gr.all, &at, &end);
-  while (at < end) {
-    const int64_t row = at / gr.all;
-    const int g0 = static_cast<int>(at - row * gr.all);
-    const int g1 = static_cast<int>(min(static_cast<int64_t>(gr.all), g0 + (end - at)));
+  for (Place w(p, gr, at, D); at < end; w.next_row(p, D)) {
+    const int g0 = w.g, g1 = static_cast<int>(min(static_cast<int64_t>(gr.all), g0 + (end - at)));
     at += g1 - g0;
-    const int64_t b = row / p.q_len, r = row - b * p.q_len;
-    const int64_t cache = (b * p.T + p.q_start + r) * p.Hkv * D;
-    const RowAngles ang(p, row, p.q_start + r);
+    const int64_t row = w.row, cache = w.cache;
+    const RowAngles ang(p, row, p.q_start + w.r);
     if (g0 < gr.q)
       fwd_heads<E, D, kNorm, kInter, U>(p, lr, ang, static_cast<const E*>(p.q_in) + row * p.q_stride,
                                 static_cast<E*>(p.q) + row * p.Hq * D, static_cast<const E*>(p.gamma_q), p.Hq, g0,
@@ -379,10 +399,14 @@ __device__ __forceinline__ void bwd_heads(const NormRopeParams& p, const LaneRot
 }
 
 // Blocks per SM and groups in flight per warp, timed together: forward (4096
-// rows, 64 + 8 + 8 heads of 128, bf16) 31.8 us with two blocks and 4 + 4
+// rows, 64 + 8 + 8 heads of 128, bf16) 31.5 us with two blocks and 4 + 4
 // groups, 34.4 without the loads ahead, 36 with 2 + 2, 37 with the next row
-// prefetched into L2; backward (2048 rows, 32 + 8 + 8 heads) 25.8 us with one
-// block and 4 groups, 28.2 with two blocks of 2, 26.2 with 6.
+// prefetched into L2; backward (2048 rows, 32 + 8 + 8 heads, dgamma included)
+// 25.2 us with one block and 4 groups, 28.2 with two blocks of 2, 26.2 with 6.
+// With the groups ahead in a shared-memory ring (cp.async) the forward took
+// 29.5 and the backward 27: even with its arithmetic and stores left out the
+// backward's 63 MB of reads took 21 us, so neither more bytes in flight nor
+// fewer instructions move it.
 constexpr int kBwdBlocksPerSm = 1;
 
 template <typename E, int D, bool kNorm, bool kInter>
@@ -397,14 +421,11 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm)
   grid_launch_dependents();
   grid_wait();
   stretch(static_cast<int64_t>(p.B) * p.q_len * gr.all, &at, &end);
-  while (at < end) {
-    const int64_t row = at / gr.all;
-    const int g0 = static_cast<int>(at - row * gr.all);
-    const int g1 = static_cast<int>(min(static_cast<int64_t>(gr.all), g0 + (end - at)));
+  for (Place w(p, gr, at, D); at < end; w.next_row(p, D)) {
+    const int g0 = w.g, g1 = static_cast<int>(min(static_cast<int64_t>(gr.all), g0 + (end - at)));
     at += g1 - g0;
-    const int64_t b = row / p.q_len, r = row - b * p.q_len;
-    const int64_t cache = (b * p.T + p.q_start + r) * p.Hkv * D;
-    const RowAngles ang(p, row, p.q_start + r);
+    const int64_t row = w.row, cache = w.cache;
+    const RowAngles ang(p, row, p.q_start + w.r);
     if (g0 < gr.q)
       bwd_heads<E, D, kNorm, kInter, U>(p, lr, ang, static_cast<const E*>(p.q_in) + row * p.q_stride, p.dq + row * p.Hq * D,
                                 static_cast<E*>(p.dq_in) + row * p.dq_stride, static_cast<const E*>(p.gamma_q), p.Hq,
