@@ -69,7 +69,7 @@ constexpr int kPartStride = 128 + 4;           // floats between rows of a split
 // narrow tile pays only where it saves a wave; a split CTA's 0.24, whatever
 // A's rows (its four MMAs are issued in about 110 cycles each).
 constexpr int64_t kPairStageCost = 510, kPairColumnCost = 98, kPairFixedCost = 13000;
-constexpr int64_t kSplitStageCost = 455, kSplitFixedCost = 11500, kSplitJoinCost = 1500;
+constexpr int64_t kSplitStageCost = 455, kSplitFixedCost = 9000, kSplitJoinCost = 1300, kSplitFirstJoinCost = 5500;
 static_assert(128 * kPartStride * 4 <= kStages * kStageBytes, "the partial tile is kept in the ring");
 
 template <bool kPair>
@@ -352,7 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_wait();             // operands, outputs and the error word belong to earlier kernels until here
   if (threadIdx.x == 0) skip_sh = error_already_set(p.err) ? 1u : 0u;
   __syncthreads();
-  cluster_sync();          // barriers of every CTA of the cluster are ready
+  const int ctas = kPair ? 2 : p.split;
+  if (ctas > 1) cluster_sync();   // barriers of every CTA of the cluster are ready
   tc_fence_after_sync();
   const uint32_t tmem = tmem_base_sh;
   // one decision for the cluster, so that no CTA waits for one that left
@@ -362,7 +363,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tile_n = kPair ? p.tile_n : S::kTN;
   const Tiles tiles = {(p.m + S::kTM - 1) / S::kTM, (p.n + tile_n - 1) / tile_n};
   const int all_stages = (p.k + kTK - 1) / kTK;
-  const int ctas = kPair ? 2 : p.split;
   const int first_tile = blockIdx.x / ctas;
   const int tile_step = gridDim.x / ctas;
   const int n_tiles = tiles.m * tiles.n;
@@ -449,6 +449,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t leader_empty[2] = {cluster_map(smem_u32(&bars.acc_empty[0]), kPair ? 0 : rank),
                                       cluster_map(smem_u32(&bars.acc_empty[1]), kPair ? 0 : rank)};
     uint8_t* box = smem + kOffBox + (warp - 2) * kBoxBytes;    // this warp's 4 KB
+    // bf16 results of a whole contraction go straight out; sums of several
+    // buffers or CTAs pass through registers
+    const bool direct = kMode != kLinearWgrad && (kPair || ctas == 1);
     int c = 0;
     bool ok = true;
     for (int t = first_tile; ok && t < n_tiles; t += tile_step) {
@@ -456,8 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tiles.at(t, &tm, &tn);
       const int64_t row = static_cast<int64_t>(tm) * S::kTM + tile_row;
       const int col = tn * tile_n + half * warp_cols;
-      constexpr bool kSum = kMode == kLinearWgrad || !kPair;   // the warp's columns pass through registers
-      if constexpr (kSum) {
+      if (!direct) {
         float acc[S::kColsPerWarp];
         for (int s = 0; ok && s < n_st; s += chunk, ++c) {
           if (!(ok = warp_wait(wd, &bars.acc_full[c & 1], (c >> 1) & 1))) break;
@@ -543,9 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  cluster_sync();          // nothing of this cluster touches another CTA's shared memory or TMEM from here,
-                           // but the split's reads of the partial tiles below
-  if constexpr (!kPair) {
+  // nothing of this cluster touches another CTA's shared memory or TMEM from
+  // here, but the split's reads of the partial tiles below
+  if (ctas > 1) cluster_sync();
+  if (!kPair && (kMode == kLinearWgrad || ctas > 1)) {
     // an aborted CTA's part is missing: every CTA then leaves its share out
     bool whole = !skip;
     for (int i = 0; i < ctas; ++i)
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       });
     }
-    cluster_sync();        // the parts have been read
+    if (ctas > 1) cluster_sync();   // the parts have been read
   }
   if (warp == 1) {
     tc_fence_after_sync();
@@ -663,7 +666,7 @@ cudaError_t plan_mode(LinearParams& p) {
     const int fit = (*split_fit)[c];
     if (fit < 1 || small > INT32_MAX / kMaxSplit) continue;
     const int64_t cost = ((small + fit - 1) / fit) * ((stages + c - 1) / c * kSplitStageCost + kSplitFixedCost) +
-                         (c - 1) * kSplitJoinCost;
+                         (c > 1 ? kSplitFirstJoinCost + (c - 2) * kSplitJoinCost : 0);
     if (cost < best) {
       best = cost;
       p.clusters = static_cast<int>(small);
