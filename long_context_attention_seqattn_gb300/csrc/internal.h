@@ -97,9 +97,12 @@ struct LinearParams {
   void* out;                   // bf16 (forward, dgrad) or float32 accumulator (wgrad)
   int64_t ldr, ldz, ldo;       // row strides in elements
   // filled by plan_linear_bf16
-  int split;                   // CTAs that share a tile (split shape), 0: pair shape
-  int tile_n;                  // columns of a tile (pair shape)
-  int clusters;                // clusters launched
+  int pair_tiles, tile_n;      // tiles of the pair shape and their columns
+  int pairs;                   // pairs that run at once
+  int split_tiles, split;      // small tiles and the CTAs that share one: the
+                               // whole result, or the quarters of what the pairs leave
+  // filled by the launch: this kernel's tiles, and the pairs' first tile it quarters (-1: none)
+  int tiles, tail_base;
   uint32_t a_bytes;            // bytes of one A tile's copies (split shape)
   int a_blocked, b_blocked;    // MN-major operand's map has its 64-column blocks as a dimension
   unsigned int* err;

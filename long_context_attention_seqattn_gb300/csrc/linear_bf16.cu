@@ -25,7 +25,8 @@
 //          the i-th part of the contraction, the parts meet in distributed
 //          shared memory and are added in order.  For results with few tiles
 //          (few rows, down to a single token's, or a small weight gradient),
-//          where the pairs would leave most SMs idle.
+//          where the pairs would leave most SMs idle, and for the last tiles
+//          of a larger one when they would keep the pairs for a whole wave.
 // Warps of a CTA:
 //   warp 0      TMA producer (A and B tile of a stage, 16 KB each)
 //   warp 1      TMEM owner + MMA issuer (pair: the even CTA's thread for both)
@@ -70,6 +71,7 @@ constexpr int kPartStride = 128 + 4;           // floats between rows of a split
 // A's rows (its four MMAs are issued in about 110 cycles each).
 constexpr int64_t kPairStageCost = 510, kPairColumnCost = 98, kPairFixedCost = 13000;
 constexpr int64_t kSplitStageCost = 455, kSplitFixedCost = 9000, kSplitJoinCost = 1300, kSplitFirstJoinCost = 5500;
+constexpr int64_t kSecondLaunchCost = 3000;
 static_assert(128 * kPartStride * 4 <= kStages * kStageBytes, "the partial tile is kept in the ring");
 
 template <bool kPair>
@@ -233,9 +235,12 @@ __device__ __forceinline__ void finish_block(const LinearParams& p, uint8_t* box
   }
 }
 
-template <int kMode, typename F>
+// f with the activation as a constant.  Kernels without one (kActs false) do
+// not carry the others' code: a short call's time is partly that of fetching
+// its instructions.
+template <bool kActs, typename F>
 __device__ __forceinline__ void with_act(int act, F&& f) {
-  if constexpr (kMode == kLinearWgrad) {
+  if constexpr (!kActs) {
     f(std::integral_constant<int, kActNone>());
   } else {
     switch (act) {
@@ -292,9 +297,22 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
 
 // Tile t of the result.  Bands of 8 tile rows, rows fastest within a band:
 // the tiles in flight form a block of the result, whose operands L2 serves.
+// With `quarters`, t counts the 128 x 128 quarters of the 256 x 256 tiles from
+// `base` on (the pairs' last tiles, left to split clusters).
 struct Tiles {
   int m, n;
+  bool quarters;
+  int base;
   __device__ __forceinline__ void at(int t, int* tm, int* tn) const {
+    if (quarters) {
+      whole(base + t / 4, tm, tn);
+      *tm = 2 * *tm + (t & 1);
+      *tn = 2 * *tn + ((t >> 1) & 1);
+    } else {
+      whole(t, tm, tn);
+    }
+  }
+  __device__ __forceinline__ void whole(int t, int* tm, int* tn) const {
     const int band = 8 * n;
     const int b = t / band, r = t - b * band;
     const int rows = min(8, m - 8 * b);
@@ -303,7 +321,7 @@ struct Tiles {
   }
 };
 
-template <int kMode, bool kPair>
+template <int kMode, bool kPair, bool kActs>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_bf16_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                        const __grid_constant__ CUtensorMap map_out, const __grid_constant__ LinearParams p) {
@@ -338,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&map_a);
     prefetch_tensormap(&map_b);
-    if (kMode == kLinearWgrad && kPair) prefetch_tensormap(&map_out);
+    if (kMode == kLinearWgrad) prefetch_tensormap(&map_out);
   }
   grid_launch_dependents();
   if (warp == 1) {
@@ -353,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) skip_sh = error_already_set(p.err) ? 1u : 0u;
   __syncthreads();
   const int ctas = kPair ? 2 : p.split;
+  const bool join = !kPair && ctas > 1;   // parts of a tile's sum meet at the end
   if (ctas > 1) cluster_sync();   // barriers of every CTA of the cluster are ready
   tc_fence_after_sync();
   const uint32_t tmem = tmem_base_sh;
@@ -361,11 +380,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- this cluster's tiles and this CTA's part of the contraction
   const int tile_n = kPair ? p.tile_n : S::kTN;
-  const Tiles tiles = {(p.m + S::kTM - 1) / S::kTM, (p.n + tile_n - 1) / tile_n};
+  const bool quarters = !kPair && p.tail_base >= 0;
+  const int grain_m = quarters ? 256 : S::kTM, grain_n = quarters ? 256 : tile_n;
+  const Tiles tiles = {(p.m + grain_m - 1) / grain_m, (p.n + grain_n - 1) / grain_n, quarters, p.tail_base};
   const int all_stages = (p.k + kTK - 1) / kTK;
   const int first_tile = blockIdx.x / ctas;
   const int tile_step = gridDim.x / ctas;
-  const int n_tiles = tiles.m * tiles.n;
+  const int n_tiles = p.tiles;
   // split: parts of the contraction as even as whole stages allow
   const int s_begin = kPair ? 0 : static_cast<int>(static_cast<int64_t>(all_stages) * rank / ctas);
   const int s_end = kPair ? all_stages : static_cast<int>(static_cast<int64_t>(all_stages) * (rank + 1) / ctas);
@@ -449,9 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t leader_empty[2] = {cluster_map(smem_u32(&bars.acc_empty[0]), kPair ? 0 : rank),
                                       cluster_map(smem_u32(&bars.acc_empty[1]), kPair ? 0 : rank)};
     uint8_t* box = smem + kOffBox + (warp - 2) * kBoxBytes;    // this warp's 4 KB
-    // bf16 results of a whole contraction go straight out; sums of several
-    // buffers or CTAs pass through registers
-    const bool direct = kMode != kLinearWgrad && (kPair || ctas == 1);
+    // sums of several result buffers or CTAs pass through registers, bf16
+    // results of a whole contraction go straight out
+    const bool direct = kMode != kLinearWgrad && !join;
     int c = 0;
     bool ok = true;
     for (int t = first_tile; ok && t < n_tiles; t += tile_step) {
@@ -478,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_cluster(leader_empty[c & 1]);
         }
         if (!ok) break;
-        if constexpr (kPair) {
+        if (!join) {
           // dw += the tile, 32 x 32 at a time through this warp's box: TMA adds
           // it in L2 (float32, one addition an element), clipped at dw's edges
           const int row0 = static_cast<int>(row) - lane;
@@ -508,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         if (!(ok = warp_wait(wd, &bars.acc_full[c & 1], (c >> 1) & 1))) break;
         tc_fence_after_sync();
-        with_act<kMode>(p.act, [&](auto act) {
+        with_act<kActs>(p.act, [&](auto act) {
 #pragma unroll 1
           for (int c0 = 0; c0 < warp_cols; c0 += 32) {
             uint32_t r[32];
@@ -524,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++c;
       }
     }
-    if (kMode == kLinearWgrad && kPair && lane == 0) bulk_wait_group<0>();   // every addition has been made
+    if (kMode == kLinearWgrad && lane == 0) bulk_wait_group<0>();   // every addition has been made
   }
 
   tc_fence_before_sync();
@@ -548,17 +569,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   // nothing of this cluster touches another CTA's shared memory or TMEM from
   // here, but the split's reads of the partial tiles below
   if (ctas > 1) cluster_sync();
-  if (!kPair && (kMode == kLinearWgrad || ctas > 1)) {
+  if (join) {
     // an aborted CTA's part is missing: every CTA then leaves its share out
     bool whole = !skip;
     for (int i = 0; i < ctas; ++i)
       whole = whole && ld_cluster_u32(cluster_map(smem_u32(const_cast<int*>(&abort_flag)), i)) == 0u;
     int tm, tn;
     tiles.at(first_tile, &tm, &tn);
-    const int rows = min(128, p.m - tm * 128);
-    const int groups = min(128, p.n - tn * 128) / 8;           // of eight columns
+    const int rows = max(0, min(128, p.m - tm * 128));            // (a quarter may lie past the edge)
+    const int groups = max(0, min(128, p.n - tn * 128)) / 8;      // of eight columns
     if (whole) {
-      with_act<kMode>(p.act, [&](auto act) {
+      with_act<kActs>(p.act, [&](auto act) {
         for (int u = static_cast<int>(rank) * kThreads + threadIdx.x; u < rows * groups; u += ctas * kThreads) {
           const int r = u / groups, g = u - r * groups;
           const uint32_t at = smem_u32(smem) + static_cast<uint32_t>((r * kPartStride + 8 * g) * 4);
@@ -568,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       });
     }
-    if (ctas > 1) cluster_sync();   // the parts have been read
+    cluster_sync();        // the parts have been read
   }
   if (warp == 1) {
     tc_fence_after_sync();
@@ -629,59 +650,87 @@ int widest_cluster(const Residency& r, int count, int64_t most) {
 }
 
 // Chooses the shape for p.m x p.n with contraction p.k: the one, and the tile
-// width or split, whose waves of tiles take the least time in the cost model.
-template <int kMode>
+// width or split, whose waves of tiles take the least time in the cost model;
+// or pairs for the whole waves and split clusters for the quarters of the
+// tiles that are left (501 x 4104 x 10248: 82 tiles on 76 pairs).
+template <int kMode, bool kActs>
 cudaError_t plan_mode(LinearParams& p) {
   static Residency pair_table[kMaxDevices], split_table[kMaxDevices];
   const Residency *pair_fit = nullptr, *split_fit = nullptr;
-  cudaError_t e = look_up(linear_bf16_kernel<kMode, true>, kThreads, kSmemAlloc, pair_table, &pair_fit);
+  cudaError_t e = look_up(linear_bf16_kernel<kMode, true, kActs>, kThreads, kSmemAlloc, pair_table, &pair_fit);
   if (e != cudaSuccess) return e;
-  if ((e = look_up(linear_bf16_kernel<kMode, false>, kThreads, kSmemAlloc, split_table, &split_fit)) != cudaSuccess)
+  if ((e = look_up(linear_bf16_kernel<kMode, false, kActs>, kThreads, kSmemAlloc, split_table, &split_fit)) != cudaSuccess)
     return e;
   const int pairs = (*pair_fit)[2];
   if (pairs < 1 || (*split_fit)[1] < 1) return cudaErrorLaunchOutOfResources;
   const int64_t stages = (static_cast<int64_t>(p.k) + kTK - 1) / kTK;
   p.a_bytes = kMode == kLinearWgrad ? kOperandBytes : static_cast<uint32_t>(linear_a_rows(p.m) * kTK * 2);
-  int64_t best = INT64_MAX;
+  // least time of `count` small tiles, and its split
+  auto split_cost = [&](int64_t count, int* split) {
+    int64_t least = INT64_MAX;
+    for (int c = 1; c <= kMaxSplit && c <= stages; ++c) {
+      const int fit = (*split_fit)[c];
+      if (fit < 1 || count > INT32_MAX / kMaxSplit) continue;
+      const int64_t cost = ((count + fit - 1) / fit) * ((stages + c - 1) / c * kSplitStageCost + kSplitFixedCost) +
+                           (c > 1 ? kSplitFirstJoinCost + (c - 2) * kSplitJoinCost : 0);
+      if (cost < least) {
+        least = cost;
+        *split = c;
+      }
+    }
+    return least;
+  };
+  int split = 1;
+  const int64_t small = static_cast<int64_t>((p.m + 127) / 128) * ((p.n + 127) / 128);
+  int64_t best = split_cost(small, &split);
+  p.pair_tiles = 0;
+  p.split = split;
+  p.split_tiles = static_cast<int>(small < INT32_MAX ? small : INT32_MAX);
+  p.tile_n = 256;
   // a pair copies whole tiles of A, so a result of fewer rows is left to the split shape
-  if (p.a_bytes == kOperandBytes) {
-    // widths: wgrad's epilogue adds 32-column boxes of a half; a forward whose
-    // W comes in whole blocks (see load_tile) would lose that with halves that
-    // are not (2048 x 4096 x 4096 with 240 columns: 62 us, 50 with 256)
-    const int step = kMode == kLinearDgrad || (kMode == kLinearFwd && p.n % 64 != 0) ? 16 : 128;
-    for (int tn = 256; tn >= (kMode == kLinearWgrad ? 256 : 128); tn -= step) {
-      const int64_t tiles = static_cast<int64_t>((p.m + 255) / 256) * ((p.n + tn - 1) / tn);
-      const int64_t cost =
-          ((tiles + pairs - 1) / pairs) * stages * (kPairStageCost + kPairColumnCost * (tn - 128) / 128) + kPairFixedCost;
+  if (p.a_bytes != kOperandBytes) return cudaSuccess;
+  // widths: wgrad's epilogue adds 32-column boxes of a half; a forward whose
+  // W comes in whole blocks (see load_tile) would lose that with halves that
+  // are not (2048 x 4096 x 4096 with 240 columns: 62 us, 50 with 256)
+  const int step = kMode == kLinearDgrad || (kMode == kLinearFwd && p.n % 64 != 0) ? 16 : 128;
+  for (int tn = 256; tn >= (kMode == kLinearWgrad ? 256 : 128); tn -= step) {
+    const int64_t tiles = static_cast<int64_t>((p.m + 255) / 256) * ((p.n + tn - 1) / tn);
+    const int64_t wave = stages * (kPairStageCost + kPairColumnCost * (tn - 128) / 128);
+    int64_t cost = (tiles + pairs - 1) / pairs * wave + kPairFixedCost;
+    if (cost < best) {
+      best = cost;
+      p.pair_tiles = static_cast<int>(tiles);
+      p.tile_n = tn;
+      p.split_tiles = 0;
+    }
+    const int64_t rest = tiles % pairs;
+    if (tn == 256 && tiles > pairs && rest > 0) {
+      cost = tiles / pairs * wave + kPairFixedCost + split_cost(4 * rest, &split) + kSecondLaunchCost;
       if (cost < best) {
         best = cost;
+        p.pair_tiles = static_cast<int>(tiles - rest);
         p.tile_n = tn;
-        p.clusters = static_cast<int>(tiles < pairs ? tiles : pairs);
-        p.split = 0;
+        p.split_tiles = static_cast<int>(4 * rest);
+        p.split = split;
       }
     }
   }
-  const int64_t small = static_cast<int64_t>((p.m + 127) / 128) * ((p.n + 127) / 128);
-  for (int c = 1; c <= kMaxSplit && c <= stages; ++c) {
-    const int fit = (*split_fit)[c];
-    if (fit < 1 || small > INT32_MAX / kMaxSplit) continue;
-    const int64_t cost = ((small + fit - 1) / fit) * ((stages + c - 1) / c * kSplitStageCost + kSplitFixedCost) +
-                         (c > 1 ? kSplitFirstJoinCost + (c - 2) * kSplitJoinCost : 0);
-    if (cost < best) {
-      best = cost;
-      p.clusters = static_cast<int>(small);
-      p.split = c;
-    }
-  }
+  p.pairs = pairs;
   return cudaSuccess;
 }
 
-template <int kMode>
-cudaError_t launch_mode(const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
-  if (p.split == 0)
-    return launch_overlapped(linear_bf16_kernel<kMode, true>, 2u * static_cast<unsigned>(p.clusters), kThreads,
-                             kSmemAlloc, 2, s, maps.a, maps.b, maps.out, p);
-  return launch_overlapped(linear_bf16_kernel<kMode, false>, static_cast<unsigned>(p.clusters) * p.split, kThreads,
+template <int kMode, bool kActs>
+cudaError_t launch_mode(const LinearMaps& maps, LinearParams p, cudaStream_t s) {
+  if (p.pair_tiles > 0) {
+    p.tiles = p.pair_tiles;
+    const unsigned clusters = static_cast<unsigned>(p.tiles < p.pairs ? p.tiles : p.pairs);
+    const cudaError_t e = launch_overlapped(linear_bf16_kernel<kMode, true, kActs>, 2u * clusters, kThreads, kSmemAlloc, 2, s,
+                                            maps.a, maps.b, maps.out, p);
+    if (e != cudaSuccess || p.split_tiles == 0) return e;
+  }
+  p.tail_base = p.pair_tiles > 0 ? p.pair_tiles : -1;
+  p.tiles = p.split_tiles;
+  return launch_overlapped(linear_bf16_kernel<kMode, false, kActs>, static_cast<unsigned>(p.tiles) * p.split, kThreads,
                            kSmemAlloc, static_cast<unsigned>(p.split), s, maps.a, maps.b, maps.out, p);
 }
 
@@ -799,7 +848,7 @@ __global__ void __launch_bounds__(kGvThreads)
   }
   cluster_sync();
   // 8-column groups of the R rows, dealt over the cluster's blocks
-  with_act<kLinearFwd>(p.act, [&](auto act) {
+  with_act<true>(p.act, [&](auto act) {
     for (int u = rank * kGvThreads + threadIdx.x; u < R * (kCols / 8); u += cs * kGvThreads) {
       const int r = u / (kCols / 8), c = strip * kCols + 8 * (u % (kCols / 8));
       if (r >= p.m || c >= p.n) continue;
@@ -917,20 +966,25 @@ __global__ void __launch_bounds__(kSumThreads, 3)
 
 }  // namespace
 
+// f with the mode and whether there is an activation as constants.
+template <typename F>
+static cudaError_t with_mode(int mode, int act, F&& f) {
+  if (mode == kLinearWgrad) return f(std::integral_constant<int, kLinearWgrad>(), std::false_type());
+  if (mode == kLinearFwd)
+    return act == kActNone ? f(std::integral_constant<int, kLinearFwd>(), std::false_type())
+                           : f(std::integral_constant<int, kLinearFwd>(), std::true_type());
+  return act == kActNone ? f(std::integral_constant<int, kLinearDgrad>(), std::false_type())
+                         : f(std::integral_constant<int, kLinearDgrad>(), std::true_type());
+}
+
 cudaError_t plan_linear_bf16(int mode, LinearParams& p) {
-  switch (mode) {
-    case kLinearFwd: return plan_mode<kLinearFwd>(p);
-    case kLinearDgrad: return plan_mode<kLinearDgrad>(p);
-    default: return plan_mode<kLinearWgrad>(p);
-  }
+  return with_mode(mode, p.act, [&](auto m, auto acts) { return plan_mode<decltype(m)::value, decltype(acts)::value>(p); });
 }
 
 cudaError_t launch_linear_bf16(int mode, const LinearMaps& maps, const LinearParams& p, cudaStream_t s) {
-  switch (mode) {
-    case kLinearFwd: return launch_mode<kLinearFwd>(maps, p, s);
-    case kLinearDgrad: return launch_mode<kLinearDgrad>(maps, p, s);
-    default: return launch_mode<kLinearWgrad>(maps, p, s);
-  }
+  return with_mode(mode, p.act, [&](auto m, auto acts) {
+    return launch_mode<decltype(m)::value, decltype(acts)::value>(maps, p, s);
+  });
 }
 
 cudaError_t launch_linear_gemv(const LinearParams& p, const void* x, int64_t ldx, const void* w, cudaStream_t s) {

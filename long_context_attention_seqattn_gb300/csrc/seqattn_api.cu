@@ -563,7 +563,7 @@ seqattn_status run_linear(int mode, LinearParams& p, const void* a, int64_t lda,
   memset(&maps.out, 0, sizeof(maps.out));
   // whole blocks only, and tiles (halves of a pair's) that start on one
   auto mn_map = [&](CUtensorMap* m, const void* base, int64_t mn, int64_t ld, int* blocked) {
-    *blocked = mn % 64 == 0 && (p.split > 0 || p.tile_n % 128 == 0);
+    *blocked = mn % 64 == 0 && p.tile_n % 128 == 0;
     return *blocked ? make_map_blocks(m, base, p.k, mn, ld) : make_map_2d(m, base, p.k, mn, ld, kLinearStageK);
   };
   const bool made = (mode == kLinearWgrad ? mn_map(&maps.a, a, p.m, lda, &p.a_blocked)

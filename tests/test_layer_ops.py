@@ -165,6 +165,47 @@ def test_linear_wgrad_keeps_float32_over_long_contractions():
     _within("dw", dw, ref, ((32 + 16) * 2.0 ** -23 + (rows / 512 + 2) * U_F32) * ref)
 
 
+@pytest.mark.parametrize("cols", [1800, 1856])
+def test_linear_with_several_waves_of_tiles(cols):
+    """Some 88 tiles of 256 x 256 over a long contraction: more than run at
+    once, with a rest that is computed in other shapes.  References in float64
+    on the GPU; same bits on a second run."""
+    rows, k = 2570, 4104
+    x, w = _rand(210, rows, k).cuda(), _rand(211, k, cols, std=k ** -0.5).cuda()
+    r, b = _rand(212, rows, cols).cuda(), _rand(213, cols).cuda()
+    for act, res in (("silu", r), ("none", None)):
+        outs = []
+        for _ in range(2):
+            y, z = torch.full_like(r, float("nan")), torch.full_like(r, float("nan"))
+            binding.linear_fwd(x, w, y, bias=b, act=act, residual=res, z=z)
+            outs.append((y, z))
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+        z64 = x.double() @ w.double() + b.double()
+        tol = _sum_tol(k, x.double().abs() @ w.double().abs() + b.double().abs())
+        y64 = _act64(z64, act) + (res.double() if res is not None else 0)
+        ytol = 1.13 * tol + 2.0 ** -20 * (1 + z64.abs()) if act != "none" else tol
+        if res is not None:
+            ytol = ytol + U_F32 * (y64.abs() + res.double().abs())
+        _within("z", outs[0][1], z64.cpu(), (U_BF16 * z64.abs() + tol).cpu())
+        _within("y", outs[0][0], y64.cpu(), (U_BF16 * y64.abs() + ytol).cpu())
+    # dx [2570, cols] = g [2570, 4104] wt^T
+    g, wt = x, w.t().contiguous()
+    dx = r.clone()
+    binding.linear_dgrad(g, wt, dx, residual=dx)
+    ref = g.double() @ wt.double().t() + r.double()
+    tol = _sum_tol(k, g.double().abs() @ wt.double().abs().t()) + U_F32 * (ref.abs() + r.double().abs())
+    _within("dx", dx, ref.cpu(), (U_BF16 * ref.abs() + tol).cpu())
+    # dw [2568, cols] += a^T g over 4104 rows
+    a, gg = _rand(214, k, 2568).cuda(), _rand(215, k, cols).cuda()
+    dws = [torch.zeros((2568, cols), device="cuda") for _ in range(2)]
+    for dw in dws:
+        binding.linear_wgrad(a, gg, dw)
+    assert torch.equal(*dws)
+    mags = a.double().abs().t() @ gg.double().abs()
+    _within("dw", dws[0], (a.double().t() @ gg.double()).cpu(),
+            (((32 + 16) * 2.0 ** -23 + (k / 512 + 2) * U_F32) * mags).cpu())
+
+
 def test_linear_strided_operands_and_neighbours():
     """Rows of wider matrices: what lies between and behind the rows is NaN
     and must neither be read into the result nor written."""
