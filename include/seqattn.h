@@ -231,7 +231,8 @@ typedef enum {
  *           gradient of this product's own pre-activation.
  *   wgrad:  dbias may be NULL.
  * residual may be the output itself (same pointer and stride); no other
- * overlap of an output with an input is allowed.  Requires k, n and every
+ * overlap of an output with an operand is allowed (INVALID_ARG where two start
+ * at the same address).  Requires k, n and every
  * stride to be positive multiples of 8, strides at least the row length,
  * pointers 16-byte aligned, 0 <= rows < 2^31 - 512; rows == 0 is a no-op.
  * Strides of operands that are NULL are ignored.  No workspace.  Async on
@@ -280,7 +281,7 @@ typedef struct {
  *     or NULL for position q_start + r on every axis.
  *   q (out) [B, q_len, Hq, d]; k_cache, v_cache (out rows) [B, T, Hkv, d].
  * The strides are at least a row's length and multiples of 8 elements;
- * eps >= 0.  Sums, angles and the rotation are in float32, rounded once.
+ * eps >= 0.  Outputs overlap no other operand.  Sums, angles and the rotation are in float32, rounded once.
  */
 seqattn_status seqattn_qk_norm_rope_fwd(const seqattn_problem* pb, int64_t q_start, int64_t q_len,
                                         const void* q_in, int64_t ld_q, const void* k_in,
@@ -302,6 +303,8 @@ seqattn_status seqattn_qk_norm_rope_fwd(const seqattn_problem* pb, int64_t q_sta
  *   workspace: device scratch of seqattn_qk_norm_rope_bwd_workspace_size(pb)
  *     bytes, 256-byte aligned, when there is a norm (else NULL, 0); calls that
  *     overlap need one each, and must not update the same dgamma.
+ * Outputs overlap no other operand; dgamma_q and dgamma_k are two vectors, also
+ * when one gamma is used for both (their sum is its gradient).
  */
 seqattn_status seqattn_qk_norm_rope_bwd(const seqattn_problem* pb, int64_t q_start, int64_t q_len,
                                         const void* q_in, int64_t ld_q, const void* k_in,

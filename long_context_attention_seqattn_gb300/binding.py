@@ -343,7 +343,8 @@ def linear_fwd(x, w, y, bias=None, act="none", residual=None, z=None, stream=Non
     """y = act(x w + bias) + residual, rounded to bf16 once.  ``x`` [..., k],
     ``y``, ``residual`` [..., n] bf16 with rows at a uniform stride, ``w``
     [k, n] and ``bias`` [n] bf16.  ``z`` [..., n] bf16, if given, receives the
-    pre-activation x w + bias.  ``residual`` may be ``y``."""
+    pre-activation x w + bias.  ``residual`` may be ``y``; no other operand
+    may overlap an output."""
     status = (_marshal or _native()).linear_fwd(x, w, y, bias, _act_code(act), residual, z, stream)
     if status:
         _check(status)
@@ -428,7 +429,8 @@ def qk_norm_rope_bwd(q_in, k_in, dq, dk_accum, dv_accum, dq_in, dk_in, dv_in, q_
     ``k_in`` are the forward's inputs and ``dgamma_q``, ``dgamma_k`` [d]
     float32 are accumulated; ``workspace`` is a uint8 CUDA tensor of at least
     ``qk_norm_rope_bwd_workspace_size(d)`` bytes (allocated here when
-    omitted).  ``dv_accum`` and ``dv_in`` may both be None."""
+    omitted).  ``dv_accum`` and ``dv_in`` may both be None.  ``dgamma_q`` and
+    ``dgamma_k`` are two tensors even when one gamma serves both."""
     temp = workspace is None and stream is not None and gamma_q is not None
     if temp:
         workspace = torch.empty(qk_norm_rope_bwd_workspace_size(dq.shape[-1]), dtype=torch.uint8, device=dq.device)
@@ -441,6 +443,19 @@ def qk_norm_rope_bwd(q_in, k_in, dq, dk_accum, dv_accum, dq_in, dk_in, dv_in, q_
         workspace.record_stream(stream)       # as in chunk_bwd
 
 
+def _collide(outs, ins):
+    """Whether any of the address ranges ``outs`` (start, bytes) meets another
+    one of them or one of ``ins``."""
+    end_out = end_any = 0
+    for start, size, out in sorted([(a, n, True) for a, n in outs] + [(a, n, False) for a, n in ins]):
+        if size and start < (end_any if out else end_out):
+            return True
+        end_any = max(end_any, start + size)
+        if out:
+            end_out = max(end_out, start + size)
+    return False
+
+
 class AdamW:
     """AdamW over many tensors, one launch a step (a few for hundreds of
     tensors).  ``params``: float32 master weights; ``grads``: their gradients
@@ -450,7 +465,8 @@ class AdamW:
     for each 256 elements: m, and the square root of v.  The states are
     allocated zeroed, or taken from ``m``, ``v`` (and ``m_scale``,
     ``v_scale``), lists as long as ``params``.  ``weight_decay``: one number
-    or one per tensor.  All tensors contiguous, on one device."""
+    or one per tensor.  All tensors contiguous, on one device; none that a step
+    writes overlaps another."""
 
     def __init__(self, params, grads, lowp=None, state_bits=32, weight_decay=0.0, m=None, v=None, m_scale=None,
                  v_scale=None):
@@ -498,6 +514,10 @@ class AdamW:
                     raise ValueError(f"{name}[{i}] must have {size} elements on {self.device}")
             self._tensors[i] = AdamwTensor(_addr(p), _addr(lo), _addr(g), _addr(mi), _addr(vi), _addr(ms), _addr(vs),
                                            n, float(wd), int(g.dtype == torch.bfloat16))
+        extent = lambda ts: [(t.data_ptr(), t.numel() * t.element_size()) for t in ts if t is not None]
+        if _collide(extent(self.params + self.lowp + self.m + self.v + self.m_scale + self.v_scale),
+                    extent(self.grads)):
+            raise ValueError("a tensor that the step writes overlaps another one of params, grads, lowp or the states")
 
     def step(self, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, grad_scale=1.0, stream=None):
         """One step; ``step`` counts from 1.  ``lr``, ``step`` and

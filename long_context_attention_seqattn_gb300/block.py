@@ -96,6 +96,8 @@ class AttentionBlock:
 
     def backward(self, dy):
         """dx from dy (bf16), after ``forward``; adds every weight's gradient to ``grads``."""
+        if tuple(dy.shape) != self.shape:
+            raise ValueError(f"dy has shape {tuple(dy.shape)}, expected {self.shape}")
         w, g, b = self.weights, self.grads, self.bufs
         dx = torch.empty_like(dy)
         binding.reset_accum(b.dk, b.dv, self.heads[0])

@@ -107,11 +107,10 @@ __device__ __forceinline__ float act_value(float z) {
 
 // Past |z| = 128 every derivative is 0 or 1 in float32; taking the limit there
 // keeps infinite intermediate products (0 * inf) out of the formulas.
+// (relu's is not multiplied but chosen, as 0 * inf is not 0, see times_grad.)
 template <int kAct>
 __device__ __forceinline__ float act_grad(float z) {
-  if constexpr (kAct != kActNone && kAct != kActRelu)
-    if (fabsf(z) > 128.f) return z > 0.f ? 1.f : 0.f;
-  if constexpr (kAct == kActRelu) return z > 0.f ? 1.f : 0.f;
+  if (fabsf(z) > 128.f) return z > 0.f ? 1.f : 0.f;
   if constexpr (kAct == kActSilu) {
     const float s = sigmoidf(z);
     return s * (1.f + z * (1.f - s));
@@ -122,7 +121,13 @@ __device__ __forceinline__ float act_grad(float z) {
     const float s = sigmoidf(2.f * kTanhA * (z + kTanhB * z * z * z));
     return s + z * s * (1.f - s) * 2.f * kTanhA * (1.f + 3.f * kTanhB * z * z);
   }
-  return 1.f;
+}
+
+// v act'(z); a NaN of z passes relu, as it does in the forward.
+template <int kAct>
+__device__ __forceinline__ float times_grad(float v, float z) {
+  if constexpr (kAct == kActRelu) return z > 0.f ? v : (z != z ? z : 0.f);
+  else return v * act_grad<kAct>(z);
 }
 
 __device__ __forceinline__ void unpack8(const uint4& q, float (&f)[8]) {
@@ -162,7 +167,7 @@ __device__ __forceinline__ void finish8(const LinearParams& p, int64_t row, int 
   } else if constexpr (kAct != kActNone) {
     unpack8(*reinterpret_cast<const uint4*>(p.z + row * p.ldz + col), t);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= act_grad<kAct>(t[i]);
+    for (int i = 0; i < 8; ++i) v[i] = times_grad<kAct>(v[i], t[i]);
   }
   if (p.residual != nullptr) {
     unpack8(*reinterpret_cast<const uint4*>(p.residual + row * p.ldr + col), t);
@@ -223,7 +228,7 @@ __device__ __forceinline__ void finish_block(const LinearParams& p, uint8_t* box
       } else if constexpr (kAct != kActNone) {
         unpack8(zin[i], t);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= act_grad<kAct>(t[k]);
+        for (int k = 0; k < 8; ++k) v[k] = times_grad<kAct>(v[k], t[k]);
       }
       if (p.residual != nullptr) {
         unpack8(res[i], t);

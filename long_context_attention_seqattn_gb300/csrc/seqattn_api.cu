@@ -543,6 +543,30 @@ seqattn_status check_linear(int64_t rows, int32_t k, int32_t n, int32_t act) {
   return SEQATTN_OK;
 }
 
+// Refuses outputs that start where another operand does: in-place calls that
+// the kernels, whose tiles are written while others are still read, cannot make.
+seqattn_status check_apart(std::initializer_list<std::pair<const void*, const char*>> outs,
+                           std::initializer_list<std::pair<const void*, const char*>> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    if (o->first == nullptr) continue;
+    for (auto other = o + 1; other != outs.end(); ++other)
+      if (o->first == other->first)
+        return fail(SEQATTN_ERR_INVALID_ARG, "%s and %s are the same memory", o->second, other->second);
+    for (auto& in : ins)
+      if (o->first == in.first)
+        return fail(SEQATTN_ERR_INVALID_ARG, "%s is the memory of %s", o->second, in.second);
+  }
+  return SEQATTN_OK;
+}
+
+// The residual may be the output itself, element for element.
+seqattn_status check_residual(const void* residual, int64_t ldr, const void* out, int64_t ldo) {
+  if (residual != nullptr && residual == out && ldr != ldo)
+    return fail(SEQATTN_ERR_INVALID_ARG, "the residual is the output with another row stride (%lld, %lld)", (long long)ldr,
+                (long long)ldo);
+  return SEQATTN_OK;
+}
+
 // Common end of the three linear calls: error word, wait limit, maps, launch.
 // Operand a carries the result's row index, b its column index.  An operand
 // whose contiguous dimension is that index (MN-major) is `mn` columns of
@@ -594,6 +618,10 @@ seqattn_status seqattn_linear_fwd(int64_t rows, int32_t k, int32_t n, const void
   if (s != SEQATTN_OK) return s;
   if (!aligned16(bias) || !aligned16(residual) || !aligned16(z))
     return fail(SEQATTN_ERR_INVALID_ARG, "bias, residual or z is not 16-byte aligned");
+  if ((s = check_apart({{y, "y"}, {z, "z"}}, {{x, "x"}, {w, "w"}, {bias, "bias"}})) != SEQATTN_OK ||
+      (s = check_apart({{z, "z"}}, {{residual, "residual"}})) != SEQATTN_OK ||
+      (s = check_residual(residual, ldr, y, ldy)) != SEQATTN_OK)
+    return s;
   LinearParams p = {};
   p.m = static_cast<int>(rows);
   p.n = n;
@@ -625,6 +653,9 @@ seqattn_status seqattn_linear_dgrad(int64_t rows, int32_t k, int32_t n, const vo
   if (s != SEQATTN_OK) return s;
   if (!aligned16(residual) || !aligned16(z))
     return fail(SEQATTN_ERR_INVALID_ARG, "residual or z is not 16-byte aligned");
+  if ((s = check_apart({{dx, "dx"}}, {{g, "g"}, {w, "w"}, {act != SEQATTN_ACT_NONE ? z : nullptr, "z"}})) != SEQATTN_OK ||
+      (s = check_residual(residual, ldr, dx, lddx)) != SEQATTN_OK)
+    return s;
   LinearParams p = {};
   p.m = static_cast<int>(rows);
   p.n = k;
@@ -648,6 +679,7 @@ seqattn_status seqattn_linear_wgrad(int64_t rows, int32_t k, int32_t n, const vo
   s = check_ptrs({{x, "x"}, {g, "g"}, {dw, "dw"}});
   if (s != SEQATTN_OK) return s;
   if (!aligned16(dbias)) return fail(SEQATTN_ERR_INVALID_ARG, "dbias is not 16-byte aligned");
+  if ((s = check_apart({{dw, "dw"}, {dbias, "dbias"}}, {{x, "x"}, {g, "g"}})) != SEQATTN_OK) return s;
   LinearParams p = {};
   p.m = k;
   p.n = n;
@@ -673,9 +705,11 @@ seqattn_status check_norm_rope(const seqattn_problem* pb, int64_t q_start, int64
                                const int64_t* positions, NormRopeParams* p) {
   seqattn_status s = check_problem(pb);
   if (s != SEQATTN_OK) return s;
-  if (q_start < 0 || q_len < 0 || q_start + q_len > pb->seq_capacity)
+  if (q_start < 0 || q_len < 0 || q_start > pb->seq_capacity || q_len > pb->seq_capacity - q_start)
     return fail(SEQATTN_ERR_INVALID_ARG, "need 0 <= q_start and 0 <= q_len and q_start + q_len <= seq_capacity (got %lld, %lld)",
                 (long long)q_start, (long long)q_len);
+  if (static_cast<int64_t>(pb->num_q_heads) * pb->head_dim > INT32_MAX)
+    return fail(SEQATTN_ERR_INVALID_ARG, "num_q_heads * head_dim exceeds 2^31 - 1");
   if ((gamma_q == nullptr) != (gamma_k == nullptr))
     return fail(SEQATTN_ERR_INVALID_ARG, "gamma_q and gamma_k must both be given or both be NULL");
   if (gamma_q != nullptr && !(eps >= 0.f && isfinite(eps)))
@@ -742,6 +776,9 @@ seqattn_status seqattn_qk_norm_rope_fwd(const seqattn_problem* pb, int64_t q_sta
   if (s != SEQATTN_OK) return s;
   if (!aligned16(v_in) || !aligned16(v_cache))
     return fail(SEQATTN_ERR_INVALID_ARG, "v_in or v_cache is not 16-byte aligned");
+  s = check_apart({{q, "q"}, {k_cache, "k_cache"}, {v_cache, "v_cache"}},
+                  {{q_in, "q_in"}, {k_in, "k_in"}, {v_in, "v_in"}, {gamma_q, "gamma_q"}, {gamma_k, "gamma_k"}});
+  if (s != SEQATTN_OK) return s;
   p.q_in = q_in;
   p.k_in = k_in;
   p.v_in = v_in;
@@ -784,6 +821,9 @@ seqattn_status seqattn_qk_norm_rope_bwd(const seqattn_problem* pb, int64_t q_sta
   if (s != SEQATTN_OK) return s;
   if (!aligned16(dv_accum) || !aligned16(dv_in))
     return fail(SEQATTN_ERR_INVALID_ARG, "dv_accum or dv_in is not 16-byte aligned");
+  s = check_apart({{dq_in, "dq_in"}, {dk_in, "dk_in"}, {dv_in, "dv_in"}},
+                  {{dq, "dq"}, {dk_accum, "dk_accum"}, {dv_accum, "dv_accum"}});
+  if (s != SEQATTN_OK) return s;
   if (norm) {
     s = check_ptrs({{q_in, "q_in"}, {k_in, "k_in"}, {dgamma_q, "dgamma_q"}, {dgamma_k, "dgamma_k"},
                     {workspace, "workspace"}});
@@ -791,6 +831,11 @@ seqattn_status seqattn_qk_norm_rope_bwd(const seqattn_problem* pb, int64_t q_sta
     if (workspace_size < norm_rope_workspace(pb->head_dim))
       return fail(SEQATTN_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed", workspace_size,
                   norm_rope_workspace(pb->head_dim));
+    s = check_apart({{dq_in, "dq_in"}, {dk_in, "dk_in"}, {dv_in, "dv_in"}, {dgamma_q, "dgamma_q"},
+                     {dgamma_k, "dgamma_k"}, {workspace, "workspace"}},
+                    {{q_in, "q_in"}, {k_in, "k_in"}, {gamma_q, "gamma_q"}, {gamma_k, "gamma_k"}, {dq, "dq"},
+                     {dk_accum, "dk_accum"}, {dv_accum, "dv_accum"}});
+    if (s != SEQATTN_OK) return s;
     p.q_in = q_in;
     p.k_in = k_in;
     p.q_stride = ld_q;

@@ -226,3 +226,5 @@ def test_block_refuses():
         block.forward(x.cuda()[:, :10])
     with pytest.raises(ValueError, match="positions"):
         AttentionBlock(1, 64, 64, 1, 1, 64, 32, positions=torch.zeros((1, 1, 63), dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError, match="dy has shape"):
+        block.backward(torch.zeros((x.shape[0], x.shape[1] + 8, x.shape[2]), dtype=torch.bfloat16, device="cuda"))

@@ -151,7 +151,84 @@ def test_adamw_without_work_is_a_no_op(lib):
     assert lib.seqattn_adamw_step(empty, 1, 8, _params(), None) == 0
 
 
+def _message(lib):
+    return lib.seqattn_last_error().decode()
+
+
+A = [0x100000 * (i + 2) for i in range(16)]      # fake addresses, all different
+
+
+@pytest.mark.parametrize("kw,words", [
+    (dict(y=A[0]), "y is the memory of x"), (dict(y=A[1]), "y is the memory of w"),
+    (dict(z=A[0], ldz=128), "z is the memory of x"), (dict(z=A[2], ldz=128), "y and z"),
+    (dict(residual=A[3], ldr=128, z=A[3], ldz=128), "z is the memory of residual"),
+    (dict(residual=A[2], ldr=256), "another row stride"),
+])
+def test_linear_fwd_refuses_shared_memory(lib, kw, words):
+    assert _call(lib.seqattn_linear_fwd, dict(FWD, x=A[0], w=A[1], y=A[2]), kw) == INV
+    assert words in _message(lib)
+
+
+@pytest.mark.parametrize("kw,words", [
+    (dict(dx=A[0]), "dx is the memory of g"), (dict(act=2, z=A[2], ldz=64), "dx is the memory of z"),
+    (dict(residual=A[2], ldr=128), "another row stride"),
+])
+def test_linear_dgrad_refuses_shared_memory(lib, kw, words):
+    assert _call(lib.seqattn_linear_dgrad, dict(DGRAD, g=A[0], w=A[1], dx=A[2]), kw) == INV
+    assert words in _message(lib)
+
+
+@pytest.mark.parametrize("kw,words", [(dict(dw=A[0]), "dw is the memory of x"), (dict(dbias=A[2]), "dw and dbias")])
+def test_linear_wgrad_refuses_shared_memory(lib, kw, words):
+    assert _call(lib.seqattn_linear_wgrad, dict(WGRAD, x=A[0], g=A[1], dw=A[2]), kw) == INV
+    assert words in _message(lib)
+
+
+RFWD_APART = dict(RFWD, q_in=A[0], k_in=A[1], v_in=A[2], gamma_q=A[3], gamma_k=A[3], q=A[5], k_cache=A[6],
+                  v_cache=A[7])
+RBWD_APART = dict(RBWD, q_in=A[0], k_in=A[1], gamma_q=A[2], gamma_k=A[2], dq=A[4], dk=A[5], dv=A[6], dq_in=A[7],
+                  dk_in=A[8], dv_in=A[9], dgamma_q=A[10], dgamma_k=A[11], workspace=A[12])
+
+
+@pytest.mark.parametrize("kw,words", [
+    (dict(q=A[0]), "q is the memory of q_in"), (dict(k_cache=A[1]), "k_cache is the memory of k_in"),
+    (dict(k_cache=A[7]), "k_cache and v_cache"),
+])
+def test_norm_rope_fwd_refuses_shared_memory(lib, kw, words):
+    assert _call(lib.seqattn_qk_norm_rope_fwd, RFWD_APART, kw) == INV
+    assert words in _message(lib)
+
+
+@pytest.mark.parametrize("kw,words", [
+    (dict(dgamma_k=A[10]), "dgamma_q and dgamma_k"), (dict(dq_in=A[0]), "dq_in is the memory of q_in"),
+    (dict(dk_in=A[9]), "dk_in and dv_in"), (dict(dq_in=A[4]), "dq_in is the memory of dq"),
+    (dict(workspace=A[10]), "dgamma_q and workspace"),
+])
+def test_norm_rope_bwd_refuses_shared_memory(lib, kw, words):
+    assert _call(lib.seqattn_qk_norm_rope_bwd, RBWD_APART, kw) == INV
+    assert words in _message(lib)
+
+
+@pytest.mark.parametrize("kw", [dict(q_start=2 ** 63 - 1), dict(q_len=2 ** 63 - 1, q_start=1),
+                                dict(q_start=2 ** 63 - 1, q_len=2 ** 63 - 1),
+                                dict(pb=_pb(num_q_heads=2 ** 30, num_kv_heads=1), ld_q=2 ** 36)])
+def test_norm_rope_refuses_sizes_past_their_integers(lib, kw):
+    assert _call(lib.seqattn_qk_norm_rope_fwd, RFWD_APART, kw) == INV
+    assert _call(lib.seqattn_qk_norm_rope_bwd, RBWD_APART, {k: v for k, v in kw.items()}) == INV
+
+
 # ------------------------------------------------------------------ the binding's own checks
+
+@pytest.mark.parametrize("outs,ins,want", [
+    ([(100, 10), (110, 10)], [(120, 5), (122, 5)], False),       # side by side; inputs may overlap
+    ([(100, 10), (109, 10)], [], True), ([(100, 10), (100, 10)], [], True), ([(100, 50), (120, 5)], [], True),
+    ([(100, 10)], [(95, 6)], True), ([(100, 10)], [(90, 40)], True), ([(100, 10)], [(90, 10)], False),
+    ([(100, 10)], [(104, 2)], True), ([(100, 10)], [(90, 40), (200, 5)], True), ([(0, 0), (0, 0)], [(0, 0)], False),
+    ([(100, 10), (105, 0)], [], False),
+])
+def test_ranges_that_collide(outs, ins, want):
+    assert binding._collide(outs, ins) is want
+
 
 def test_rope_plan_turns():
     """A frequency f is kept as round(f / 2 pi * 2^64) modulo a turn."""

@@ -302,6 +302,35 @@ def test_linear_special_values():
         assert dx[0].tolist() == want, (act, dx[0].tolist())
 
 
+def test_linear_dgrad_of_relu_drops_infinities():
+    """Where relu was off its gradient is zero whatever comes back; a NaN of z
+    is kept."""
+    w = torch.eye(8).bfloat16().cuda()
+    z = torch.tensor([[1.0, -1.0, 1.0, -1.0, 0.0, float("nan"), -float("inf"), float("inf")]]).bfloat16()
+    g = torch.full((1, 8), 2.0).bfloat16()
+    g_inf = torch.full((1, 8), float("inf")).bfloat16()
+    for rows in (1, 130):
+        dx = torch.empty((rows, 8), dtype=torch.bfloat16, device="cuda")
+        zz = z.expand(rows, 8).contiguous().cuda()
+        binding.linear_dgrad(g.expand(rows, 8).contiguous().cuda(), w, dx, act="relu", z=zz)
+        assert torch.isnan(dx[:, 5]).all()
+        assert dx[0, [0, 1, 2, 3, 4, 6, 7]].tolist() == [2, 0, 2, 0, 0, 0, 2]
+        # infinite and NaN products (inf * 0)
+        binding.linear_dgrad(g_inf.expand(rows, 8).contiguous().cuda(), w, dx, act="relu", z=zz)
+        assert dx[0, [1, 3, 4, 6]].tolist() == [0, 0, 0, 0]
+
+
+def test_adamw_refuses_tensors_that_overlap():
+    buf, g = torch.zeros(64, device="cuda"), torch.zeros(32, device="cuda")
+    a, b = buf[:32], buf[16:48]
+    binding.AdamW([a, buf[32:]], [g, g])                         # one gradient for two tensors is only read
+    for params, grads, kw in (([a, a], [g, g], {}), ([a, b], [g, g], {}), ([a], [b], {}),
+                              ([a], [g], dict(m=[buf[32:]], v=[buf[32:]])),
+                              ([a], [g], dict(lowp=[a.view(torch.bfloat16)[:32]]))):
+        with pytest.raises(ValueError, match="overlaps"):
+            binding.AdamW(params, grads, **kw)
+
+
 def test_linear_is_reproducible_and_replays():
     """Same bits on every run, on another stream and from a replayed graph
     with new inputs in the same buffers."""
