@@ -170,9 +170,9 @@ seqattn_status check_chunk(const seqattn_problem* pb, int64_t q_start, int64_t q
   if (q_start < 0 || prefix_len < 0 || prefix_len > q_start)
     return fail(SEQATTN_ERR_INVALID_ARG, "need 0 <= prefix_len <= q_start (got %lld, %lld)",
                 (long long)prefix_len, (long long)q_start);
-  if (q_start + q_len > pb->seq_capacity)
-    return fail(SEQATTN_ERR_INVALID_ARG, "q_start + q_len = %lld exceeds seq_capacity %lld",
-                (long long)(q_start + q_len), (long long)pb->seq_capacity);
+  if (q_start > pb->seq_capacity || q_len > pb->seq_capacity - q_start)     // (their sum may pass int64)
+    return fail(SEQATTN_ERR_INVALID_ARG, "q_start + q_len = %lld + %lld exceeds seq_capacity %lld", (long long)q_start,
+                (long long)q_len, (long long)pb->seq_capacity);
   if (!(scale > 0.f) || !isfinite(scale))
     return fail(SEQATTN_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
   if (static_cast<int64_t>(pb->batch) * q_len > INT32_MAX)

@@ -217,6 +217,15 @@ def test_norm_rope_refuses_sizes_past_their_integers(lib, kw):
     assert _call(lib.seqattn_qk_norm_rope_bwd, RBWD_APART, {k: v for k, v in kw.items()}) == INV
 
 
+@pytest.mark.parametrize("q_start,q_len", [(2 ** 63 - 1, 1), (1, 2 ** 63 - 1), (2 ** 63 - 1, 2 ** 63 - 1), (1009, 16)])
+def test_chunk_calls_refuse_rows_past_the_cache(lib, q_start, q_len):
+    pb = _pb()
+    assert lib.seqattn_chunk_fwd(pb, q_start, q_len, 0, 0.1, P, P, P, P, P, None) == INV
+    assert "exceeds seq_capacity" in _message(lib)
+    assert lib.seqattn_chunk_bwd(pb, q_start, q_len, 0, 0.1, P, P, P, P, P, P, P, P, P, P, 2 ** 62, None) == INV
+    assert "exceeds seq_capacity" in _message(lib)
+
+
 # ------------------------------------------------------------------ the binding's own checks
 
 @pytest.mark.parametrize("outs,ins,want", [
