@@ -144,36 +144,53 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-// Eight consecutive columns of one result row.
+// What else eight consecutive columns of a result row need from memory, so
+// that it can be loaded ahead of their sum.
+struct Extra {
+  uint4 a = {}, b = {};   // forward: bias, residual; dgrad: z, residual; wgrad: the old dw
+  template <int kMode>
+  __device__ __forceinline__ void load(const LinearParams& p, int64_t row, int col) {
+    if constexpr (kMode == kLinearWgrad) {
+      const uint4* o = reinterpret_cast<const uint4*>(static_cast<float*>(p.out) + row * p.ldo + col);
+      a = o[0], b = o[1];
+    } else {
+      if constexpr (kMode == kLinearFwd) {
+        if (p.bias != nullptr) a = __ldg(reinterpret_cast<const uint4*>(p.bias + col));
+      } else {
+        if (p.act != kActNone) a = *reinterpret_cast<const uint4*>(p.z + row * p.ldz + col);
+      }
+      if (p.residual != nullptr) b = *reinterpret_cast<const uint4*>(p.residual + row * p.ldr + col);
+    }
+  }
+};
+
+// Eight consecutive columns of one result row (an absent bias or residual is
+// zeros: x + 0 is x).
 template <int kMode, int kAct>
-__device__ __forceinline__ void finish8(const LinearParams& p, int64_t row, int col, float (&v)[8]) {
+__device__ __forceinline__ void finish8(const LinearParams& p, int64_t row, int col, const Extra& extra, float (&v)[8]) {
   float t[8];
   if constexpr (kMode == kLinearWgrad) {
     float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.ldo + col);
-    const float4 a = o[0], b = o[1];
-    o[0] = make_float4(a.x + v[0], a.y + v[1], a.z + v[2], a.w + v[3]);
-    o[1] = make_float4(b.x + v[4], b.y + v[5], b.z + v[6], b.w + v[7]);
+    o[0] = make_float4(__uint_as_float(extra.a.x) + v[0], __uint_as_float(extra.a.y) + v[1],
+                       __uint_as_float(extra.a.z) + v[2], __uint_as_float(extra.a.w) + v[3]);
+    o[1] = make_float4(__uint_as_float(extra.b.x) + v[4], __uint_as_float(extra.b.y) + v[5],
+                       __uint_as_float(extra.b.z) + v[6], __uint_as_float(extra.b.w) + v[7]);
     return;
   }
+  unpack8(extra.a, t);
   if constexpr (kMode == kLinearFwd) {
-    if (p.bias != nullptr) {
-      unpack8(__ldg(reinterpret_cast<const uint4*>(p.bias + col)), t);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += t[i];
-    }
+    for (int i = 0; i < 8; ++i) v[i] += t[i];
     if (p.z != nullptr) *reinterpret_cast<uint4*>(p.z + row * p.ldz + col) = pack8(v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = act_value<kAct>(v[i]);
   } else if constexpr (kAct != kActNone) {
-    unpack8(*reinterpret_cast<const uint4*>(p.z + row * p.ldz + col), t);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = times_grad<kAct>(v[i], t[i]);
   }
-  if (p.residual != nullptr) {
-    unpack8(*reinterpret_cast<const uint4*>(p.residual + row * p.ldr + col), t);
+  unpack8(extra.b, t);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += t[i];
-  }
+  for (int i = 0; i < 8; ++i) v[i] += t[i];
   *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * p.ldo + col) = pack8(v);
 }
 
@@ -259,13 +276,22 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 }
 
 // v += the eight floats at shared address `at` of every CTA of the cluster, in
-// rank order.
+// rank order, four CTAs' loads in flight.
 __device__ __forceinline__ void add_parts(uint32_t at, int ctas, float (&v)[8]) {
-  for (int i = 0; i < ctas; ++i) {
-    const uint32_t from = cluster_map(at, static_cast<uint32_t>(i));
-    const float4 x = ld_cluster_v4(from), y = ld_cluster_v4(from + 16);
-    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-    v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+  for (int i0 = 0; i0 < ctas; i0 += 4) {
+    float4 x[4] = {}, y[4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i0 + i < ctas) {
+        const uint32_t from = cluster_map(at, static_cast<uint32_t>(i0 + i));
+        x[i] = ld_cluster_v4(from);
+        y[i] = ld_cluster_v4(from + 16);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[0] += x[i].x, v[1] += x[i].y, v[2] += x[i].z, v[3] += x[i].w;
+      v[4] += y[i].x, v[5] += y[i].y, v[6] += y[i].z, v[7] += y[i].w;
+    }
   }
 }
 
@@ -338,7 +364,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   __shared__ LinearBarriers bars;
   __shared__ uint32_t tmem_base_sh;
-  __shared__ uint32_t skip_sh;
   __shared__ int abort_flag;
   Watchdog wd(&abort_flag, p.err, p.wait_cycles);
 
@@ -372,16 +397,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_relinquish();
     }
   }
-  grid_wait();             // operands, outputs and the error word belong to earlier kernels until here
-  if (threadIdx.x == 0) skip_sh = error_already_set(p.err) ? 1u : 0u;
-  __syncthreads();
-  const int ctas = kPair ? 2 : p.split;
-  const bool join = !kPair && ctas > 1;   // parts of a tile's sum meet at the end
-  if (ctas > 1) cluster_sync();   // barriers of every CTA of the cluster are ready
+  // barriers and TMEM are ready, for a pair those of both CTAs; the CTAs of a
+  // split cluster work by themselves until their parts meet
+  if constexpr (kPair) cluster_sync();
+  else __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = tmem_base_sh;
-  // one decision for the cluster, so that no CTA waits for one that left
-  const bool skip = ld_cluster_u32(cluster_map(smem_u32(&skip_sh), 0)) != 0u;
+  const int ctas = kPair ? 2 : p.split;
+  const bool join = !kPair && ctas > 1;   // parts of a tile's sum meet at the end
+  grid_wait();             // operands, outputs and the error word belong to earlier kernels until here
 
   // ---- this cluster's tiles and this CTA's part of the contraction
   const int tile_n = kPair ? p.tile_n : S::kTN;
@@ -399,9 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int chunk = kMode == kLinearWgrad ? kChunkStages : n_st;   // stages of one result buffer
   int n_issued = 0;
 
-  if (skip) {
-    // leave together below
-  } else if (warp == 0) {
+  if (warp == 0) {
     if (lane == 0) {
       int it = 0;
       bool ok = true;
@@ -479,7 +501,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // results of a whole contraction go straight out
     const bool direct = kMode != kLinearWgrad && !join;
     int c = 0;
-    bool ok = true;
+    // After an earlier error nothing is written, and the CTA gives up.  Asked
+    // here, under the first loads: before them it would cost their start 0.5 us.
+    bool ok = !error_already_set(p.err);
+    if (!ok) *wd.abort_flag = 1;
     for (int t = first_tile; ok && t < n_tiles; t += tile_step) {
       int tm, tn;
       tiles.at(t, &tm, &tn);
@@ -555,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before_sync();
   __syncthreads();
-  if (wd.aborted() && !skip) {
+  if (wd.aborted()) {
     // a wait ran out: let the copies already in flight land first.  The odd
     // CTA of a pair has them counted on the even one's barrier, whose phases
     // it cannot rely on now: it gives them 100 us instead.
@@ -571,36 +596,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
+  if constexpr (!kPair)
+    if (warp == 1) {
+      tc_fence_after_sync();
+      tmem_dealloc(tmem, S::kTmemCols);
+    }
+  // ---- the split's join: units of eight columns of a row, dealt over the
+  // cluster's threads.  What a thread's first unit needs from memory is loaded
+  // while the other CTAs' parts are waited for.
+  int join_row = 0, join_col = 0, groups = 1, units = 0, unit = 0;
+  Extra extra;
+  if (join) {
+    int tm, tn;
+    tiles.at(first_tile, &tm, &tn);
+    join_row = 128 * tm, join_col = 128 * tn;
+    groups = max(1, min(128, p.n - join_col) / 8);
+    units = max(0, min(128, p.m - join_row)) * max(0, min(128, p.n - join_col) / 8);   // (a quarter may lie past the edge)
+    unit = static_cast<int>(rank) * kThreads + threadIdx.x;
+    if (unit < units) extra.load<kMode>(p, join_row + unit / groups, join_col + 8 * (unit % groups));
+  }
   // nothing of this cluster touches another CTA's shared memory or TMEM from
   // here, but the split's reads of the partial tiles below
   if (ctas > 1) cluster_sync();
   if (join) {
     // an aborted CTA's part is missing: every CTA then leaves its share out
-    bool whole = !skip;
-    for (int i = 0; i < ctas; ++i)
-      whole = whole && ld_cluster_u32(cluster_map(smem_u32(const_cast<int*>(&abort_flag)), i)) == 0u;
-    int tm, tn;
-    tiles.at(first_tile, &tm, &tn);
-    const int rows = max(0, min(128, p.m - tm * 128));            // (a quarter may lie past the edge)
-    const int groups = max(0, min(128, p.n - tn * 128)) / 8;      // of eight columns
-    if (whole) {
-      with_act<kActs>(p.act, [&](auto act) {
-        for (int u = static_cast<int>(rank) * kThreads + threadIdx.x; u < rows * groups; u += ctas * kThreads) {
-          const int r = u / groups, g = u - r * groups;
-          const uint32_t at = smem_u32(smem) + static_cast<uint32_t>((r * kPartStride + 8 * g) * 4);
-          float v[8] = {};
-          add_parts(at, ctas, v);
-          finish8<kMode, decltype(act)::value>(p, static_cast<int64_t>(tm) * 128 + r, tn * 128 + 8 * g, v);
-        }
-      });
-    }
+    uint32_t lost = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxSplit; ++i)
+      if (i < ctas) lost |= ld_cluster_u32(cluster_map(smem_u32(const_cast<int*>(&abort_flag)), i));
+    with_act<kActs>(p.act, [&](auto act) {
+      for (; unit < units; unit += ctas * kThreads) {
+        const int r = unit / groups, g = unit - r * groups;
+        float v[8] = {};
+        add_parts(smem_u32(smem) + static_cast<uint32_t>((r * kPartStride + 8 * g) * 4), ctas, v);
+        if (lost != 0u) break;
+        finish8<kMode, decltype(act)::value>(p, join_row + r, join_col + 8 * g, extra, v);
+        const int next = unit + ctas * kThreads;
+        if (next < units) extra.load<kMode>(p, join_row + next / groups, join_col + 8 * (next % groups));
+      }
+    });
     cluster_sync();        // the parts have been read
   }
-  if (warp == 1) {
-    tc_fence_after_sync();
-    if constexpr (kPair) tmem_dealloc_pair(tmem, S::kTmemCols);
-    else tmem_dealloc(tmem, S::kTmemCols);
-  }
+  if constexpr (kPair)
+    if (warp == 1) {
+      tc_fence_after_sync();
+      tmem_dealloc_pair(tmem, S::kTmemCols);
+    }
 }
 
 // How many clusters of each size a kernel's launch has on the device at once,
@@ -851,18 +892,19 @@ __global__ void __launch_bounds__(kGvThreads)
     for (int g = 0; g < kGvThreads / 32; ++g) t += part[g][i / kCols][i % kCols];
     part[0][i / kCols][i % kCols] = t;
   }
+  // 8-column groups of the R rows, the first threads of the cluster's first block
+  static_assert(R * (kCols / 8) <= kGvThreads, "a group a thread");
+  const int out_row = threadIdx.x / (kCols / 8), out_col = strip * kCols + 8 * (threadIdx.x % (kCols / 8));
+  const bool writes = rank == 0 && out_row < R && out_row < p.m && out_col < p.n;
+  Extra extra;
+  if (writes) extra.load<kLinearFwd>(p, out_row, out_col);
   cluster_sync();
-  // 8-column groups of the R rows, dealt over the cluster's blocks
-  with_act<true>(p.act, [&](auto act) {
-    for (int u = rank * kGvThreads + threadIdx.x; u < R * (kCols / 8); u += cs * kGvThreads) {
-      const int r = u / (kCols / 8), c = strip * kCols + 8 * (u % (kCols / 8));
-      if (r >= p.m || c >= p.n) continue;
-      const uint32_t at = smem_u32(&part[0][r][c - strip * kCols]);
+  if (writes)
+    with_act<true>(p.act, [&](auto act) {
       float v[8] = {};
-      add_parts(at, cs, v);
-      finish8<kLinearFwd, decltype(act)::value>(p, r, c, v);
-    }
-  });
+      add_parts(smem_u32(&part[0][out_row][out_col - strip * kCols]), cs, v);
+      finish8<kLinearFwd, decltype(act)::value>(p, out_row, out_col, extra, v);
+    });
   cluster_sync();                          // the other blocks have read this one's part
 }
 

@@ -415,6 +415,31 @@ def test_linear_waits_run_out_and_recover(rows, k, n):
     _within("dw", dw, ref, 50 * 2.0 ** -23 * (x.double().cpu().abs().t() @ g.double().cpu().abs()))
 
 
+@pytest.mark.parametrize("rows,k,n", [(40, 512, 264), (300, 64, 136), (2570, 520, 1800)])
+def test_linear_writes_nothing_after_an_error(rows, k, n):
+    """Calls that find the error word set leave their outputs alone, and the
+    next ones after it has been read and cleared are whole."""
+    x, w, g = _rand(63, rows, k).cuda(), _rand(64, k, n, std=k ** -0.5).cuda(), _rand(65, rows, n).cuda()
+    y, dx, dw = torch.full_like(g, 7.0), torch.full_like(x, 7.0), torch.full((k, n), 7.0, device="cuda")
+    first = torch.empty_like(g)
+    binding.sync_status()
+    try:
+        binding.set_wait_limit(1)
+        binding.linear_fwd(x, w, first)
+    finally:
+        binding.set_wait_limit(0)
+    binding.linear_fwd(x, w, y)
+    binding.linear_dgrad(g, w, dx)
+    binding.linear_wgrad(x, g, dw)
+    with pytest.raises(binding.SeqattnError):
+        binding.sync_status()
+    assert (y == 7).all() and (dx == 7).all() and (dw == 7).all()
+    binding.linear_fwd(x, w, y)
+    binding.sync_status()
+    ref = x.double() @ w.double()
+    _within("y", y, ref.cpu(), (U_BF16 * ref.abs() + _sum_tol(k, x.double().abs() @ w.double().abs())).cpu())
+
+
 # ============================================================== head norm + rotary positions
 
 def _angles(positions, inv_freq, axis):
