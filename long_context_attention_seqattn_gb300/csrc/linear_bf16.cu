@@ -68,9 +68,17 @@ constexpr int kPartStride = 128 + 4;           // floats between rows of a split
 // every SM busy: a pair's stage 0.32 us with a tile of 256 columns and 0.27
 // with 128 (kPairStageCost, and kPairColumnCost for 128 columns more), so a
 // narrow tile pays only where it saves a wave; a split CTA's 0.24, whatever
-// A's rows (its four MMAs are issued in about 110 cycles each).
-constexpr int64_t kPairStageCost = 510, kPairColumnCost = 98, kPairFixedCost = 13000;
-constexpr int64_t kSplitStageCost = 455, kSplitFixedCost = 9000, kSplitJoinCost = 1300, kSplitFirstJoinCost = 5500;
+// A's rows (its four MMAs are issued in about 110 cycles each).  A join costs
+// more for tiles of more rows.  The constants are fitted: over 100 shapes of 2
+// to 2048 rows the geometric means of forward and dgrad are 6.61 and 6.57 us
+// with these, 6.67 and 6.63 with joins that cost the same whatever the rows
+// (4000 and 600; 512 x 1024 x 1024 then takes 9.8 us instead of 8.1).
+// kSecondLaunchCost: what a second launch has to save before it is made (501 x
+// 4104 x 10248 took 55 us with it and 62 without, see plan_mode).
+constexpr int64_t kPairStageCost = 510, kPairColumnCost = 98, kPairFixedCost = 12300;
+constexpr int64_t kSplitStageCost = 455, kSplitFixedCost = 8000;
+constexpr int64_t kSplitFirstJoinCost = 3500, kSplitFirstJoinRowCost = 10;   // two CTAs, and for each row of the tile
+constexpr int64_t kSplitJoinCost = 400, kSplitJoinRowCost = 5;               // each further CTA, and row
 constexpr int64_t kSecondLaunchCost = 3000;
 static_assert(128 * kPartStride * 4 <= kStages * kStageBytes, "the partial tile is kept in the ring");
 
@@ -711,6 +719,9 @@ cudaError_t plan_mode(LinearParams& p) {
   if (pairs < 1 || (*split_fit)[1] < 1) return cudaErrorLaunchOutOfResources;
   const int64_t stages = (static_cast<int64_t>(p.k) + kTK - 1) / kTK;
   p.a_bytes = kMode == kLinearWgrad ? kOperandBytes : static_cast<uint32_t>(linear_a_rows(p.m) * kTK * 2);
+  const int64_t rows = p.m < 128 ? p.m : 128;      // of a small tile
+  const int64_t first_join = kSplitFirstJoinCost + kSplitFirstJoinRowCost * rows;
+  const int64_t further_join = kSplitJoinCost + kSplitJoinRowCost * rows;
   // least time of `count` small tiles, and its split
   auto split_cost = [&](int64_t count, int* split) {
     int64_t least = INT64_MAX;
@@ -718,7 +729,7 @@ cudaError_t plan_mode(LinearParams& p) {
       const int fit = (*split_fit)[c];
       if (fit < 1 || count > INT32_MAX / kMaxSplit) continue;
       const int64_t cost = ((count + fit - 1) / fit) * ((stages + c - 1) / c * kSplitStageCost + kSplitFixedCost) +
-                           (c > 1 ? kSplitFirstJoinCost + (c - 2) * kSplitJoinCost : 0);
+                           (c > 1 ? first_join + (c - 2) * further_join : 0);
       if (cost < least) {
         least = cost;
         *split = c;
