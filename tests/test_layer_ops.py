@@ -19,6 +19,9 @@ adamw     float32 states: at most 8 roundings of a term each.  8-bit states:
 """
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -964,3 +967,41 @@ def test_all_operators_on_two_streams_at_once():
     for a, b in zip(alone, together):
         for name in a:
             assert torch.equal(a[name], b[name]), name
+
+
+def test_first_calls_may_be_captured():
+    """In a new process, calls that have never run are captured into a graph
+    and replayed."""
+    code = """
+import torch
+from long_context_attention_seqattn_gb300 import binding
+def new(*shape):
+    return torch.randn(shape, device="cuda").bfloat16()
+xs, w = [new(r, 512) for r in (1, 40, 2570)], new(512, 1800) / 32
+ys = [torch.zeros(len(x), 1800, device="cuda", dtype=torch.bfloat16) for x in xs]
+dw = torch.zeros_like(w, dtype=torch.float32)
+qkv = new(1, 64, 6, 128)
+q, k, v = (torch.zeros(1, 64, h, 128, device="cuda", dtype=torch.bfloat16) for h in (4, 1, 1))
+p, g = torch.zeros(1000, device="cuda"), torch.ones(1000, device="cuda")
+opt = binding.AdamW([p], [g], state_bits=8)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    for x, y in zip(xs, ys):
+        binding.linear_fwd(x, w, y)
+    binding.linear_wgrad(xs[1], ys[1], dw)
+    binding.qk_norm_rope_fwd(*qkv.split((4, 1, 1), 2), q, k, v, 0, plan=binding.rope_plan([0.0] * 64))
+    opt.step(0.5, 1)
+graph.replay()
+binding.sync_status()
+for x, y in zip(xs, ys):
+    ref = x.double() @ w.double()
+    assert ((y - ref).abs() <= 2.0 ** -8 * ref.abs() + 48 * 2.0 ** -23 * (x.double().abs() @ w.double().abs())).all()
+ref = xs[1].double().t() @ ys[1].double()
+assert ((dw - ref).abs() <= 50 * 2.0 ** -23 * (xs[1].double().abs().t() @ ys[1].double().abs())).all()
+assert torch.equal(torch.cat((q, k, v), 2), qkv)
+assert torch.allclose(p, torch.full_like(p, -0.5), rtol=2.0 ** -20)    # 16 roundings
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
